@@ -26,12 +26,17 @@ ERRORS = {
     -7: "EPDC_ERR_HIP",
 }
 EXPORTS = ("epdc_dispatch_scratch_bytes", "epdc_dispatch", "epdc_dispatch_noalloc", "epdc_combine",
-           "epdc_landing_rows", "epdc_combine_push", "epdc_combine_reduce", "epdc_last_error")
+           "epdc_landing_rows", "epdc_combine_push", "epdc_combine_reduce", "epdc_last_error",
+           "epdc_route", "epdc_route_grad", "epdc_mx_scale_dim", "epdc_mx_quantize", "epdc_mx_dequantize",
+           "epdc_group_scratch_bytes", "epdc_group_experts", "epdc_expert_product")
 # include/epdc.h: the dispatch scratch's status word (index in 32-bit words) and its values
 EPDC_STATUS_WORD = 2
 EPDC_STATUS_WAIT_TIMEOUT = 1
 EPDC_STATUS_ROW_OUTSIDE = 2
 EPDC_MAX_SCALE_DIM = 1024
+EPDC_SOFTMAX, EPDC_SIGMOID = 0, 1
+EPDC_MAX_ROUTE_EXPERTS = 1024
+EPDC_MAX_GROUP_EXPERTS = 1024
 
 
 class EpdcError(RuntimeError):
@@ -54,7 +59,29 @@ class EpCfg(ctypes.Structure):
     ]
 
     def __repr__(self):
-        return "EpCfg(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+        return type(self).__name__ + "(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class RouteCfg(ctypes.Structure):
+    """epdc_route_cfg: a router."""
+    _fields_ = [
+        ("numExperts", ctypes.c_int32),
+        ("numExpertPerToken", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("numGroups", ctypes.c_int32),
+        ("groupsPerToken", ctypes.c_int32),
+        ("groupTop", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("routedScale", ctypes.c_float),
+    ]
+
+    def __init__(self, numExperts=0, numExpertPerToken=0, dtype=EPDC_BF16, score=EPDC_SOFTMAX, numGroups=1,
+                 groupsPerToken=1, groupTop=1, renormalize=0, routedScale=1.0):
+        super().__init__(numExperts, numExpertPerToken, dtype, score, numGroups, groupsPerToken, groupTop, renormalize,
+                         routedScale)
+
+    __repr__ = EpCfg.__repr__
 
 
 _lib = None
@@ -84,6 +111,23 @@ def load_library() -> ctypes.CDLL:
     lib.epdc_combine_push.argtypes = [cfgp, i32] + [p] * 6 + [p]
     lib.epdc_combine_reduce.restype = ctypes.c_int
     lib.epdc_combine_reduce.argtypes = [cfgp, i32] + [p] * 5 + [i32, p]
+    routep = ctypes.POINTER(RouteCfg)
+    lib.epdc_route.restype = ctypes.c_int
+    lib.epdc_route.argtypes = [routep, i32] + [p] * 5
+    lib.epdc_route_grad.restype = ctypes.c_int
+    lib.epdc_route_grad.argtypes = [routep, i32] + [p] * 5
+    lib.epdc_mx_scale_dim.restype = i32
+    lib.epdc_mx_scale_dim.argtypes = [i32]
+    lib.epdc_mx_quantize.restype = ctypes.c_int
+    lib.epdc_mx_quantize.argtypes = [i32] * 4 + [p] * 5
+    lib.epdc_mx_dequantize.restype = ctypes.c_int
+    lib.epdc_mx_dequantize.argtypes = [i32] * 3 + [p] * 4 + [i32, p]
+    lib.epdc_group_scratch_bytes.restype = sz
+    lib.epdc_group_scratch_bytes.argtypes = [cfgp, i32]
+    lib.epdc_group_experts.restype = ctypes.c_int
+    lib.epdc_group_experts.argtypes = [cfgp, i32] + [p] * 8 + [sz, p]
+    lib.epdc_expert_product.restype = ctypes.c_int
+    lib.epdc_expert_product.argtypes = [i32] * 5 + [p] * 8 + [i32, p]
     lib.epdc_last_error.restype = ctypes.c_char_p
     lib.epdc_last_error.argtypes = []
     _lib = lib

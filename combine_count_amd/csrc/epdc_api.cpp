@@ -10,13 +10,15 @@
 #include <cstdio>
 #include <string>
 
+#include "epdc_host.h"
 #include "epdc_internal.h"
 
 static_assert(EPDC_STATUS_WORD == epdc::kScratchError, "status word offset");
 static_assert(EPDC_STATUS_WAIT_TIMEOUT == epdc::kStatusWaitTimeout, "status value");
 static_assert(EPDC_STATUS_ROW_OUTSIDE == epdc::kStatusRowOutside, "status value");
 
-namespace {
+namespace epdc {
+namespace host {
 
 thread_local std::string g_lastError;
 
@@ -30,7 +32,20 @@ int fail(int code, const char *fmt, ...) {
     return code;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int hip_status(hipError_t e, const char *what) {
+    if (e == hipSuccess) return EPDC_OK;
+    return fail(EPDC_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace host
+}  // namespace epdc
+
+namespace {
+
+using epdc::host::aligned;
+using epdc::host::fail;
+using epdc::host::g_lastError;
+using epdc::host::hip_status;
 
 int32_t pow2_ceil(int32_t v) {
     int32_t r = 1;
@@ -59,10 +74,12 @@ int32_t elem_bytes(int32_t dtype, bool combine) {
     }
 }
 
-// Checks shared by both entry points (EpCfg validity: MORI JIT v2 design doc,
+}  // namespace
+
+// Checks shared by the entry points (EpCfg validity: MORI JIT v2 design doc,
 // §3.5 -- 16-byte token rows, topk and worldSize within one wavefront,
 // receive capacity covering the worst case).
-int check_cfg(const epdc_cfg *c, int32_t numTokens, bool combine) {
+int epdc::host::check_cfg(const epdc_cfg *c, int32_t numTokens, bool combine) {
     if (!c) return fail(EPDC_ERR_NULLPTR, "cfg is NULL");
     if (c->worldSize < 1 || c->worldSize > 64)
         return fail(EPDC_ERR_INVALID_ARG, "worldSize %d outside [1, 64]", c->worldSize);
@@ -99,6 +116,10 @@ int check_cfg(const epdc_cfg *c, int32_t numTokens, bool combine) {
     return EPDC_OK;
 }
 
+namespace {
+
+using epdc::host::check_cfg;
+
 size_t scratch_bytes(const epdc_cfg *c) {
     const int64_t nTiles = ((int64_t)c->maxTokPerRank + epdc::kTile - 1) / epdc::kTile;
     return (size_t)((epdc::kScratchHeaderWords + 2 * nTiles * pow2_ceil(c->worldSize)) * sizeof(uint32_t));
@@ -115,11 +136,6 @@ int32_t landing_rows(const epdc_cfg *c, int32_t numTokens) {
 // §5), independent of the rows' type.  -1 if it is neither.
 int32_t out_elem_bytes(int32_t outDtype) {
     return outDtype == EPDC_BF16 ? 2 : outDtype == EPDC_FP32 ? 4 : -1;
-}
-
-int hip_status(hipError_t e, const char *what) {
-    if (e == hipSuccess) return EPDC_OK;
-    return fail(EPDC_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // Checks of every dispatch argument but the scratch, and the kernel

@@ -19,6 +19,13 @@
  *             landing rows at offsets the dispatch hands over, then the
  *             source reduces them.  Same result as the gather combine.
  *
+ *   routing, fp4x2 quantisation, grouping by expert, the experts' product
+ *             What stands on both sides of a dispatch and a combine: the
+ *             top-k experts and weights of a token (and their gradient), the
+ *             fp4x2 wire's codes and scales, the expert-sorted list of a
+ *             window's rows, and the product of those rows with each expert's
+ *             fp4x2 weights.  Declared in the second half of this file.
+ *
  * Argument names follow EpCfg (MORI JIT v2 design doc, §3.2).  The geometry
  * fields of EpCfg (blockNum, warpPerBlock, waveSize) are not part of the ABI:
  * the library picks launch geometry itself.
@@ -283,6 +290,205 @@ int epdc_combine_push(const epdc_cfg *cfg, int32_t numTokens,
 int epdc_combine_reduce(const epdc_cfg *cfg, int32_t numTokens,
                         const void *landing, const float *landScale, const int32_t *recvCount,
                         const int32_t *sendMap, void *out, int32_t outDtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Routing
+ * ------------------------------------------------------------------------ */
+
+/* How logits become scores. */
+typedef enum {
+    EPDC_SOFTMAX = 0, /* s = exp(l - max l) / sum over the token's experts */
+    EPDC_SIGMOID = 1  /* s = 1 / (1 + exp(-l))                             */
+} epdc_score;
+
+/* Largest numExperts of a router. */
+#define EPDC_MAX_ROUTE_EXPERTS 1024
+
+/* A router.
+ *   numExperts         E, 1..EPDC_MAX_ROUTE_EXPERTS
+ *   numExpertPerToken  K, 1..64, at most groupsPerToken * E / numGroups
+ *   dtype              logits' (and their gradient's) type: EPDC_BF16 or EPDC_FP32
+ *   score              epdc_score
+ *   numGroups          G, 1..64, divides E: group g holds experts [g*E/G, (g+1)*E/G)
+ *   groupsPerToken     1..G: a token's experts come from its best groups (G: no limit)
+ *   groupTop           1 or 2, at most E/G: a group's score is the sum of that many of
+ *                      its best choice values
+ *   renormalize        1: a token's K weights are divided by their sum; 0: not
+ *   routedScale        finite; the weights are multiplied by it */
+typedef struct epdc_route_cfg {
+    int32_t numExperts;
+    int32_t numExpertPerToken;
+    int32_t dtype;
+    int32_t score;
+    int32_t numGroups;
+    int32_t groupsPerToken;
+    int32_t groupTop;
+    int32_t renormalize;
+    float routedScale;
+} epdc_route_cfg;
+
+/*
+ * Route numTokens tokens (numTokens >= 0): their K best experts and weights.
+ *
+ * Inputs (device, read only):
+ *   logits     [T][E] of cfg->dtype
+ *   bias       [E] fp32 or NULL (zeros): added to the scores where experts are
+ *              chosen, not in the weights (a bias that balances the experts)
+ * Outputs (device):
+ *   expertIds  [T][K] int32, best first: what epdc_dispatch takes
+ *   weights    [T][K] fp32
+ *
+ * An expert whose logit is NaN or -inf, or whose choice value s + bias is NaN
+ * or -inf, is masked: it is never chosen (a masked logit also leaves the
+ * softmax's sum).  A logit of +inf takes the softmax's whole mass, shared with
+ * the token's other +inf logits.  Experts are ordered by choice value s + bias
+ * -- with bias NULL by the logit, of which s is an increasing function -- and
+ * groups by their score (with bias NULL and groupTop 1, by their best logit;
+ * members that are masked add nothing, a group of masked members is never
+ * kept).  Ties go to the lower index.  The values are compared as computed in
+ * 64 bits, so the choice does not depend on how a 32-bit exponential rounds.
+ * Where fewer than K experts can be chosen, the slots left hold expert id -1
+ * (a dropped slot for epdc_dispatch) and weight 0.
+ * weights = routedScale * s, or routedScale * s / (sum of the K chosen s)
+ * with renormalize (0 if that sum is 0).
+ */
+int epdc_route(const epdc_route_cfg *cfg, int32_t numTokens, const void *logits, const float *bias,
+               int32_t *expertIds, float *weights, void *stream);
+
+/*
+ * Gradient of epdc_route's weights with respect to its logits.
+ *
+ * cfg's groups are ignored (the choice of experts has no gradient), and so
+ * has the bias none.  Inputs (device, read only): logits [T][E] of
+ * cfg->dtype; expertIds [T][K] as epdc_route gave them (an id outside [0, E),
+ * or of a masked logit, is a slot with weight 0 and no gradient; an id may
+ * appear in several slots); dWeights [T][K] fp32.  Output (device): dLogits
+ * [T][E] of cfg->dtype, every element written.
+ * With c = routedScale, g = dWeights, s the scores and r_k = s_k / (sum of the
+ * token's chosen s): dLogits_i is
+ *   softmax                 s_i (c g_i - sum_j c g_j s_j)  (g_i = 0 for an i not chosen)
+ *   softmax, renormalize    c r_i (g_i - sum_j g_j r_j)
+ *   sigmoid                 c s_i (1 - s_i) g_i
+ *   sigmoid, renormalize    c r_i (1 - s_i) (g_i - sum_j g_j r_j)
+ * summed over i's slots, and 0 (but for softmax without renormalize) where i
+ * has none.  Computed in fp32 and rounded once (nearest, ties to even).
+ */
+int epdc_route_grad(const epdc_route_cfg *cfg, int32_t numTokens, const void *logits,
+                    const int32_t *expertIds, const float *dWeights, void *dLogits, void *stream);
+
+/* ------------------------------------------------------------------------
+ * fp4x2 rows with block scales (OCP microscaling, MXFP4)
+ *
+ * A row of C elements (C a multiple of 32) is C/2 bytes, each two e2m1 codes
+ * (sign, 2 exponent bits, 1 mantissa bit: 0 0.5 1 1.5 2 3 4 6), the first
+ * element in the low half, and one scale byte b per 32 elements, worth
+ * 2^(b-127) (255: NaN).  The scale bytes of a row fill S =
+ * epdc_mx_scale_dim(C) 32-bit words, block i in byte i (in memory order), the
+ * bytes behind the last block 127.  So a quantised row is an EPDC_FP4X2 row of
+ * hiddenDim C/2 with scaleDim S: epdc_dispatch carries both as they are.
+ * ------------------------------------------------------------------------ */
+
+/* Scale words of a row of cols elements, ceil(cols / 128); -1 if cols is not a
+ * positive multiple of 32, or beyond 128 * EPDC_MAX_SCALE_DIM. */
+int32_t epdc_mx_scale_dim(int32_t cols);
+
+/*
+ * Quantise rows.  x is [numWindows][rowsPerWindow][cols] of dtype (EPDC_BF16
+ * or EPDC_FP32, 16-byte aligned).  Outputs: q [numWindows][rowsPerWindow]
+ * [cols/2] bytes and scales [numWindows][rowsPerWindow][S] words, q 16-byte
+ * and scales 4-byte aligned.  rowCount [numWindows] (device int32, or NULL for
+ * all rows): only rows r < rowCount[w] of window w are read and written, as of
+ * a dispatch's windows and recvCount.
+ * A block's scale byte is clamp(floor(log2 m) + 125, 0, 254), m the block's
+ * largest magnitude (0 for a block of zeros); its codes are the elements
+ * divided by the scale, to the nearest value, ties to the even code,
+ * magnitudes beyond 6 to 6.  A block that holds a NaN or an infinity gets
+ * scale byte 255 (NaN) and codes 0.
+ */
+int epdc_mx_quantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, int32_t dtype, const void *x,
+                     const int32_t *rowCount, void *q, void *scales, void *stream);
+
+/* The values of quantised rows (epdc_mx_quantize's q, scales and rowCount) as
+ * out [numWindows][rowsPerWindow][cols] of outDtype (EPDC_BF16 or EPDC_FP32, 16-byte
+ * aligned): code value times scale, exact in both types (infinite past their
+ * range, NaN where the scale byte is 255). */
+int epdc_mx_dequantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, const void *q, const void *scales,
+                       const int32_t *rowCount, void *out, int32_t outDtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Grouping received rows by expert
+ * ------------------------------------------------------------------------ */
+
+/* Largest numExpertPerRank of a grouping. */
+#define EPDC_MAX_GROUP_EXPERTS 1024
+
+/* Bytes of device scratch epdc_group_experts needs, or 0 if cfg or rank is
+ * invalid.  The scratch needs no initial contents; calls that may run at the
+ * same time need one each. */
+size_t epdc_group_scratch_bytes(const epdc_cfg *cfg, int32_t rank);
+
+/*
+ * The (row, slot) pairs of receive windows, sorted by expert.
+ *
+ * rank in [0, W): the W windows are what PE `rank` received, one window per
+ * source, and the Epr experts of that PE are grouped (group e is expert
+ * rank*Epr + e; G = Epr groups).  rank = -1: window p is what PE p received
+ * from one source, as epdc_dispatch wrote it, and every PE's experts are
+ * grouped over its own window (group e is expert e; G = E groups).
+ * Inputs (device, read only):
+ *   expertIds  [W][M][K] int32: as recvExpertIds
+ *   weights    [W][M][K] fp32: as recvWeights; NULL iff useWeights == 0
+ *   recvCount  [W] int32 valid rows per window (clamped to [0, M]), or NULL: M each
+ * A slot (w, r, k) with r < recvCount[w] whose expert is one of those its
+ * window is grouped over is an entry; entries are numbered by expert, then by
+ * window, row and slot.
+ * Outputs (device):
+ *   offsets      [G+1] int32: group e holds entries [offsets[e], offsets[e+1])
+ *   entryRow     [W*M*K] int32: the entry's flat row w*M + r
+ *   entryWeight  [W*M*K] fp32: its weight; NULL iff useWeights == 0
+ *   entryOf      [W][M][K] int32: the slot's entry, -1 for every other slot,
+ *                rows past recvCount included.  It is a sendMap into the
+ *                entries' rows: epdc_combine with worldSize 1, maxTokPerRank
+ *                W*M*K and numTokens W*M sums each row's entries.
+ *   entryRow and entryWeight past the last entry are left untouched.
+ * hiddenDim, dtype and scaleDim of cfg are not used but checked.
+ * EPDC_ERR_INVALID_ARG if W*M*K exceeds 2^31-1 or rank is outside [-1, W);
+ * EPDC_ERR_UNSUPPORTED if Epr exceeds EPDC_MAX_GROUP_EXPERTS.
+ */
+int epdc_group_experts(const epdc_cfg *cfg, int32_t rank, const int32_t *expertIds, const float *weights,
+                       const int32_t *recvCount, int32_t *offsets, int32_t *entryRow, float *entryWeight,
+                       int32_t *entryOf, void *scratch, size_t scratchBytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' product
+ * ------------------------------------------------------------------------ */
+
+/*
+ * out[i] = w_i * (rows[r_i] . weights[e]^T) for every entry i of every group e.
+ *
+ * numExperts groups of entries, offsets [numExperts+1] int32 (group e holds
+ * entries [offsets[e], offsets[e+1]); values are clamped to [0, maxEntries]).
+ * rows [numRows][hiddenDim/2] with rowScales [numRows][S] and weights
+ * [numExperts][numCols][hiddenDim/2] with weightScales [numExperts][numCols][S]
+ * are fp4x2 rows as epdc_mx_quantize makes them (S =
+ * epdc_mx_scale_dim(hiddenDim)); hiddenDim counts elements, a multiple of 32.
+ * entryRow [maxEntries] int32 is the row r_i of entry i (NULL: r_i = i); an
+ * entry whose row is outside [0, numRows) counts as a row of zeros.
+ * entryWeight [maxEntries] fp32 is w_i (NULL: 1).
+ * out [maxEntries][numCols] of outDtype (EPDC_BF16 or EPDC_FP32); its rows
+ * must be a multiple of 16 bytes; rows from offsets[numExperts] on (and rows
+ * before offsets[0]) are left untouched.
+ * Products and sums are fp32 (their order is fixed for given sizes: results
+ * are the same from run to run); w_i is applied to the sum, then the result is
+ * rounded (nearest, ties to even).  rows, weights and out must be 16-byte
+ * aligned, the other arrays 4-byte.
+ * maxEntries also chooses the kernel: pass the number of entries that can
+ * occur, not a far larger capacity, for the best speed.
+ */
+int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
+                        int32_t numRows, const void *rows, const void *rowScales, const int32_t *offsets,
+                        const int32_t *entryRow, const float *entryWeight, const void *weights,
+                        const void *weightScales, void *out, int32_t outDtype, void *stream);
 
 /* Message for the last failing call on this thread ("" if none).  The
  * pointer stays valid until the next epdc_* call on the same thread.  MORI
