@@ -284,8 +284,9 @@ int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, 
         P.numRows = numRows;
         P.rowBytes = hiddenDim / 2;
         P.words = scale_dim(hiddenDim);
-        P.rows = static_cast<const uint8_t *>(rows);
-        P.rowScales = static_cast<const uint8_t *>(rowScales);
+        // with no rows every entry is a row of zeros; what is loaded in its place is a weight row
+        P.rows = static_cast<const uint8_t *>(numRows > 0 ? rows : weights);
+        P.rowScales = static_cast<const uint8_t *>(numRows > 0 ? rowScales : weightScales);
         P.offsets = offsets;
         P.entryRow = entryRow;
         P.entryWeight = entryWeight;

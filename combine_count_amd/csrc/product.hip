@@ -17,10 +17,38 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the instruction's operand format
 
+// SA, SB: which byte of sa, sb holds the lane's scale.
+template <int SA, int SB>
 __device__ __forceinline__ f32x4 mfma_fp4(u32x4 a, u32x4 b, f32x4 c, int32_t sa, int32_t sb) {
     const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const i32x8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, kFp4, kFp4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, kFp4, kFp4, SA, sa, SB, sb);
+}
+
+// The same, the sums in accumulation registers that it updates in place, and in
+// the order written (the compiler's own allocation of 64 such sums moved them
+// between register files inside the loop).  The compiler does not see the
+// matrix instruction: its operands must not come from a vector instruction
+// just before it, and its results are read behind mfma_done().
+template <int SA, int SB>
+__device__ __forceinline__ void mfma_fp4_inplace(f32x4 &c, u32x4 a, u32x4 b, int32_t sa, int32_t sb) {
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
+}
+__device__ __forceinline__ void mfma_done() { asm volatile("s_nop 15\n\ts_nop 15"); }
+
+template <int I>
+struct Const {
+    static constexpr int value = I;
+};
+// f(Const<0>), ..., f(Const<N-1>): the instruction's byte choices are constants.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F &&f) {
+    if constexpr (I < N) {
+        f(Const<I>{});
+        each<N, I + 1>(f);
+    }
 }
 
 // Entries of expert e, both ends inside [0, maxEntries].
@@ -67,7 +95,7 @@ __global__ __launch_bounds__(256) void product_simple_kernel(ProductParams P) {
                 u32x4 av = {0, 0, 0, 0};
                 int32_t sa = 127;
                 if (kin && in[i]) av = load16<false>(a[i] + at), sa = as[i][at >> 4];
-                acc[i] = mfma_fp4(av, bv, acc[i], sa, sb);
+                acc[i] = mfma_fp4<0, 0>(av, bv, acc[i], sa, sb);
             }
         }
 #pragma unroll
@@ -87,10 +115,391 @@ __global__ __launch_bounds__(256) void product_simple_kernel(ProductParams P) {
     }
 }
 
+typedef uint32_t u32x4_dword __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at 4-byte alignment
+
+// 16 bytes per lane from memory into LDS at lds + lane * 16 (lds the same in
+// all lanes), counted by vmcnt: from rs' base at voff (per lane) + soff.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, uint32_t voff, int32_t soff, uint8_t *lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)lds, 16, (int)voff, soff, 0, 0);
+}
+__device__ __forceinline__ void load_lds16(const uint8_t *src, uint8_t *lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, 0xffffffff, 0x00020000);
+}
+
+// What goes between the products of a half besides the reads of the next.
+constexpr int kRequest = 1, kScales = 2;
+
+// Where a block's tile lies: expert, entries [m0, hi), columns from n0.
+struct TileAt {
+    int32_t e, m0, hi, n0;
+};
+
+// Tile of block b among all experts' tiles (BM entries x BN columns), or
+// e = -1 when there are fewer.  Each XCD (b % 8) takes a contiguous stretch of
+// the tiles, so the tiles that run on it together share operands in its L2;
+// within an expert, up to four row tiles go through the columns together.
+template <int BM, int BN>
+__device__ __forceinline__ TileAt find_tile(const ProductParams &P, int32_t b) {
+    const int lane = threadIdx.x & 63;
+    const int32_t NT = ceil_div(P.N, BN);
+    int64_t total = 0;
+    for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
+        int32_t lo = 0, hi = 0;
+        if (e0 + lane < P.E) group_range(P, e0 + lane, lo, hi);
+        total += __shfl(wave_incl_scan((hi - lo + BM - 1) / BM), 63);
+    }
+    total *= NT;
+    const int64_t per = (total + 7) / 8;
+    const int64_t at = (b & 7) * per + (b >> 3);
+    TileAt t;
+    t.e = -1;
+    if ((b >> 3) >= per || at >= total) return t;
+    int64_t before = 0;
+    for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
+        int32_t lo = 0, hi = 0;
+        if (e0 + lane < P.E) group_range(P, e0 + lane, lo, hi);
+        const int32_t mt = (hi - lo + BM - 1) / BM;
+        const int32_t incl = wave_incl_scan(mt);
+        const uint64_t past = __ballot((before + incl) * NT > at);
+        if (past) {
+            const int f = __builtin_ctzll(past);
+            const int32_t tiles = __shfl(mt, f);
+            int32_t r = (int32_t)(at - (before + __shfl(incl, f) - tiles) * NT);  // tile inside the expert
+            const int32_t band = r / (4 * NT), rows = min(4, tiles - band * 4);
+            r -= band * 4 * NT;
+            const int32_t n = r / rows, m = band * 4 + r - n * rows;
+            t.e = e0 + f;
+            t.m0 = __shfl(lo, f) + m * BM;
+            t.hi = min(__shfl(hi, f), t.m0 + BM);
+            t.n0 = n * BN;
+            return t;
+        }
+        before += __shfl(incl, 63);
+    }
+    return t;
+}
+
+// A BM x BN tile by four waves, each (BM/2) x (BN/2); the weights are the
+// instruction's rows, the entries its columns, so a lane ends with runs of 8
+// consecutive output columns of one entry.
+//
+// Steps of 256 elements (128 bytes a row) go through two LDS buffers, loaded
+// by the memory pipeline itself (no registers on the way).  A step is two
+// halves of 128 elements; the operands of a half are read into registers
+// during the half before:
+//     read half 1 of step k        | products of half 0
+//     wait: step k+1 has arrived (requested one whole step ago); barrier
+//     request step k+2 into step k's buffer
+//     read half 0 of step k+1      | products of half 1
+// LDS rows are 128 bytes: the 16-byte pieces of a row are stored at piece ^
+// (row's place among eight), so that the 16 lanes that read one piece of 16
+// rows spread over all banks.
+// Scale bytes: 4 words a row cover two steps; they go through registers into
+// a small LDS array, from which a lane reads the one byte its product needs.
+//
+// WIDE: the array of rows passes 32-bit offsets.
+template <int BM, int BN, bool OUT32, bool WIDE>
+__global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_kernel(ProductParams P) {
+    constexpr int FM = BM / 32, FN = BN / 32;      // 16-wide fragments of a wave
+    constexpr int LM = BM / 32, LN = BN / 32;      // LDS loads of a wave per step (8 rows each)
+    constexpr int SR = (BM + BN) / 256;            // scale rows staged per thread
+    __shared__ __attribute__((aligned(16))) uint8_t mbuf0[BM * 128], mbuf1[BM * 128], nbuf0[BN * 128], nbuf1[BN * 128];
+    // scale bytes [step pair][word][byte][fragments by four][row in the fragment][fragment of the four]
+    constexpr int kQuads = (BM + BN) / 64;
+    __shared__ __attribute__((aligned(16))) uint8_t sc[2][4][4][kQuads][16][4];
+    TileAt T = find_tile<BM, BN>(P, blockIdx.x);
+    if (uniform(T.e) < 0) return;
+    T = TileAt{uniform(T.e), uniform(T.m0), uniform(T.hi), uniform(T.n0)};  // so that the compiler knows
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int r16 = lane & 15, kb = lane >> 4;
+    const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+
+    // Row of entry m0 + i, -1 where it is none of the array's; entries behind the tile's last repeat it.
+    auto row_of = [&](int32_t i) -> int32_t {
+        const int32_t ent = min(T.m0 + i, T.hi - 1);
+        const int32_t r = P.entryRow ? P.entryRow[ent] : ent;
+        return (uint32_t)r < (uint32_t)P.numRows ? r : -1;
+    };
+    const int piece_m = ((lane & 7) ^ (lane >> 3)) * 16;
+    const int piece_n0 = ((lane & 7) ^ ((lane >> 3) & 3)) * 16, piece_n1 = piece_n0 ^ 64;
+    // Offsets of what this lane requests in a step: of the rows (their index where offsets pass 32 bits), and of the
+    // columns from the tile's first.
+    uint32_t mat[LM], nat[LN];
+    const uint8_t *nbase = P.weights + ((int64_t)T.e * P.N + T.n0) * P.rowBytes;
+    const __amdgpu_buffer_rsrc_t mrs = buffer_of(P.rows), nrs = buffer_of(nbase);
+#pragma unroll
+    for (int t = 0; t < LM; ++t) {
+        mat[t] = (uint32_t)max(row_of(wave * (BM / 4) + t * 8 + (lane >> 3)), 0);
+        if (!WIDE) mat[t] = mat[t] * (uint32_t)P.rowBytes + piece_m;
+    }
+#pragma unroll
+    for (int t = 0; t < LN; ++t)
+        nat[t] = (uint32_t)(min(wave * (BN / 4) + t * 8 + (lane >> 3), P.N - 1 - T.n0) * P.rowBytes) + (t & 1 ? piece_n1 : piece_n0);
+    const uint8_t *sptr[SR];  // scale rows this thread stages: rows of the tile first, then columns
+#pragma unroll
+    for (int t = 0; t < SR; ++t) {
+        const int i = t * 256 + tid;
+        const uint8_t *m = P.rowScales + (int64_t)max(row_of(min(i, BM - 1)), 0) * P.words * 4;
+        const uint8_t *n = P.weightScales + ((int64_t)T.e * P.N + min(T.n0 + max(i - BM, 0), P.N - 1)) * P.words * 4;
+        sptr[t] = i < BM ? m : n;
+    }
+    const int NK = (P.rowBytes + 127) / 128, blocks = P.H / 32;
+    const int tail = NK * 128 - P.rowBytes;  // bytes of the last step behind the rows' end
+
+    // Load t of the wave's LM + LN in step k.  Pieces behind the end of the rows repeat the last one (clear_tail).
+    auto request = [&](auto t, int k, uint8_t *mb, uint8_t *nb) {
+        constexpr int I = decltype(t)::value;
+        if constexpr (I < LM) {
+            uint8_t *to = mb + (wave * (BM / 4) + I * 8) * 128;
+            if constexpr (WIDE)
+                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(k * 128 + piece_m)), to);
+            else
+                load_lds16(mrs, mat[I], k * 128, to);
+        } else {
+            load_lds16(nrs, nat[I - LM], k * 128, nb + (wave * (BN / 4) + (I - LM) * 8) * 128);
+        }
+    };
+    auto request_last = [&](uint8_t *mb, uint8_t *nb) {  // step NK - 1, which the rows may end in
+        const int at = (NK - 1) * 128, last = 112 - tail;  // the last piece there is
+        each<LM>([&](auto t) {
+            constexpr int I = decltype(t)::value;
+            uint8_t *to = mb + (wave * (BM / 4) + I * 8) * 128;
+            const int piece = min(piece_m, last);
+            if constexpr (WIDE)
+                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(at + piece)), to);
+            else
+                load_lds16(mrs, mat[I] - piece_m + piece, at, to);
+        });
+        each<LN>([&](auto t) {
+            constexpr int I = decltype(t)::value;
+            const int own = I & 1 ? piece_n1 : piece_n0;
+            load_lds16(nrs, nat[I] - own + min(own, last), at, nb + (wave * (BN / 4) + I * 8) * 128);
+        });
+    };
+    // Rows that end inside the last step: zeros in the entries' pieces behind the end, once they have arrived.
+    // (The weights' pieces there hold finite values and scales: nothing adds up.)
+    auto clear_tail = [&](uint8_t *mb) {
+        if (tail == 0) return;
+#pragma unroll
+        for (int t = 0; t < LM; ++t)
+            if (piece_m >= 128 - tail)
+                *reinterpret_cast<u32x4 *>(mb + wave * (BM / 4) * 128 + t * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+        __syncthreads();
+    };
+    u32x4 sreg[SR];
+    auto scales_load = [&](int pair) {  // words 4 pair .. + 3 of the staged rows; 127 behind the row's last block
+        if (pair * 16 + 16 <= blocks) {
+#pragma unroll
+            for (int t = 0; t < SR; ++t) sreg[t] = *reinterpret_cast<const u32x4_dword *>(sptr[t] + pair * 16);
+        } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int left = blocks - pair * 16 - w * 4;  // blocks of this word
+                const uint32_t keep = left >= 4 ? 0xffffffffu : left > 0 ? (1u << (left * 8)) - 1 : 0u;
+#pragma unroll
+                for (int t = 0; t < SR; ++t) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(sptr[t] + min(pair * 4 + w, P.words - 1) * 4);
+                    sreg[t][w] = (v & keep) | (0x7f7f7f7fu & ~keep);
+                }
+            }
+        }
+    };
+    auto scale_store = [&](auto j, int pair) {  // one of the 16 SR bytes this thread stages for a pair of steps
+        constexpr int t = decltype(j)::value / 16, w = decltype(j)::value / 4 % 4, b = decltype(j)::value % 4;
+        const int i = t * 256 + tid, n = i - BM;
+        const int quad = i < BM ? i >> 6 : BM / 64 + (n >> 6);
+        const int r = i < BM ? i & 15 : ((n >> 3) & 3) * 4 + (n & 3);
+        const int f = i < BM ? (i >> 4) & 3 : ((n >> 5) & 1) * 2 + ((n >> 2) & 1);
+        sc[pair & 1][w][b][quad][r][f] = (uint8_t)(sreg[t][w] >> (8 * b));
+    };
+
+    struct Half {
+        u32x4 m[FM], n[FN];
+    };
+    struct Scales {  // of both halves of a step
+        int32_t m[2][FM / 4], n[2][FN / 4];
+    };
+    // lane's row inside a fragment: entries in order; columns so that fragments 2p and 2p + 1 of a lane join to
+    // eight in a row: column 32 p + 8 (r / 4) + 4 (f & 1) + r % 4
+    const int mrow = wm + r16, nrow = wn + (r16 >> 2) * 8 + (r16 & 3);
+    const int msw = r16 & 7, nsw = (r16 & 3) | (((r16 >> 2) & 1) << 2);
+    auto read_scales = [&](Scales &s, int k) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint8_t(*sp)[16][4] = sc[(k >> 1) & 1][(k & 1) * 2 + half][kb];
+#pragma unroll
+            for (int q = 0; q < FN / 4; ++q) s.n[half][q] = *reinterpret_cast<const int32_t *>(sp[(BM + wn) / 64 + q][r16]);
+#pragma unroll
+            for (int q = 0; q < FM / 4; ++q) s.m[half][q] = *reinterpret_cast<const int32_t *>(sp[wm / 64 + q][r16]);
+        }
+    };
+    constexpr int kReads = FM + FN;
+    // LDS read r of half `half` of a step, in the order in which the products need them.
+    auto read = [&](auto r, Half &h, const uint8_t *mb, const uint8_t *nb, int half) {
+        constexpr int R = decltype(r)::value;
+        if constexpr (R >= 1 && R <= FN) {
+            constexpr int F = R - 1;
+            h.n[F] = *reinterpret_cast<const u32x4 *>(nb + nrow * 128 + (((half * 4 + kb) ^ nsw) * 16) +
+                                                      ((F >> 1) * 32 + (F & 1) * 4) * 128);
+        } else {
+            constexpr int F = R == 0 ? 0 : R - FN;
+            h.m[F] = *reinterpret_cast<const u32x4 *>(mb + mrow * 128 + (((half * 4 + kb) ^ msw) * 16) + F * 16 * 128);
+        }
+    };
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            acc[i][j] = f32x4{0, 0, 0, 0};
+            asm volatile("" : "+a"(acc[i][j]));
+        }
+    mfma_done();
+    // The products of half HALF of a step, one matrix instruction after the other; dealt out between them, where the
+    // matrix instructions leave issue slots: the reads of the next half from mb and nb, and, by WITH, the requests of
+    // step rk into rmb and rnb or the scales of step pair rk into LDS.
+    auto multiply = [&](auto half, auto with, const Half &h, const Scales &s, Half &next, const uint8_t *mb, const uint8_t *nb,
+                        int rk, uint8_t *rmb, uint8_t *rnb) {
+        constexpr int HALF = decltype(half)::value, WITH = decltype(with)::value, kAll = FM * FN;
+        each<kAll>([&](auto q) {
+            constexpr int Q = decltype(q)::value, J = Q / FN, I = Q % FN;
+            mfma_fp4_inplace<I & 3, J & 3>(acc[I][J], h.n[I], h.m[J], s.n[HALF][I >> 2], s.m[HALF][J >> 2]);
+            constexpr int kGap = kAll / (kReads + 1) ? kAll / (kReads + 1) : 1;
+            if constexpr (Q % kGap == 0 && Q / kGap < kReads) read(Const<Q / kGap>{}, next, mb, nb, 1 - HALF);
+            if constexpr (WITH == kRequest) {
+                constexpr int kReqGap = kAll / (LM + LN);
+                if constexpr (Q % kReqGap == kReqGap / 2) request(Const<Q / kReqGap>{}, rk, rmb, rnb);
+            }
+            if constexpr (WITH == kScales && Q >= kAll * 3 / 4) {
+                constexpr int kPer = 16 * SR / (kAll / 4);
+                each<kPer>([&](auto i) { scale_store(Const<(Q - kAll * 3 / 4) * kPer + decltype(i)::value>{}, rk); });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    using First = Const<0>;
+    using Second = Const<1>;
+    using Alone = Const<0>;
+    using Request = Const<kRequest>;
+    using ScaleStore = Const<kScales>;
+    auto meet = [&] {  // this wave's LDS reads are in its registers, its requests have arrived; then all waves' have
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    Half h0, h1;
+    Scales s0, s1;  // of even and odd steps
+    scales_load(0);
+    each<16 * SR>([&](auto j) { scale_store(j, 0); });
+    if (NK == 1) {
+        request_last(mbuf0, nbuf0);
+    } else {
+        each<LM + LN>([&](auto t) { request(t, 0, mbuf0, nbuf0); });
+        if (NK == 2)
+            request_last(mbuf1, nbuf1);
+        else
+            each<LM + LN>([&](auto t) { request(t, 1, mbuf1, nbuf1); });
+    }
+    meet();
+    if (NK == 1) clear_tail(mbuf0);
+    read_scales(s0, 0);
+    each<kReads>([&](auto r) { read(r, h0, mbuf0, nbuf0, 0); });
+    int k = 0;
+    for (; k + 4 < NK; k += 2) {  // steps k and k + 1; k + 2 and k + 3, requested here, are not the last
+        multiply(First{}, Alone{}, h0, s0, h1, mbuf0, nbuf0, 0, mbuf0, nbuf0);
+        meet();
+        read_scales(s1, k + 1);
+        scales_load((k >> 1) + 1);
+        multiply(Second{}, Request{}, h1, s0, h0, mbuf1, nbuf1, k + 2, mbuf0, nbuf0);
+        multiply(First{}, ScaleStore{}, h0, s1, h1, mbuf1, nbuf1, (k >> 1) + 1, mbuf0, nbuf0);
+        meet();
+        read_scales(s0, k + 2);
+        multiply(Second{}, Request{}, h1, s1, h0, mbuf0, nbuf0, k + 3, mbuf1, nbuf1);
+    }
+    // The last one to four steps, k first.  What is read behind the last step is not used.
+    for (;; k += 2) {
+        multiply(First{}, Alone{}, h0, s0, h1, mbuf0, nbuf0, 0, mbuf0, nbuf0);
+        meet();
+        if (k + 2 == NK) clear_tail(mbuf1);
+        read_scales(s1, k + 1);
+        if (k + 2 < NK) {
+            scales_load((k >> 1) + 1);
+            if (k + 3 == NK)
+                request_last(mbuf0, nbuf0);
+            else
+                each<LM + LN>([&](auto t) { request(t, k + 2, mbuf0, nbuf0); });
+        }
+        multiply(Second{}, Alone{}, h1, s0, h0, mbuf1, nbuf1, 0, mbuf0, nbuf0);
+        if (k + 1 >= NK) break;
+        multiply(First{}, ScaleStore{}, h0, s1, h1, mbuf1, nbuf1, (k >> 1) + 1, mbuf0, nbuf0);
+        meet();
+        if (k + 3 == NK) clear_tail(mbuf0);
+        read_scales(s0, k + 2);
+        if (k + 4 == NK) request_last(mbuf1, nbuf1);
+        multiply(Second{}, Alone{}, h1, s1, h0, mbuf0, nbuf0, 0, mbuf0, nbuf0);
+        if (k + 2 >= NK) break;
+    }
+    mfma_done();
+
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int32_t ent = T.m0 + mrow + j * 16;
+        if (ent >= T.hi) continue;
+        const bool none = row_of(mrow + j * 16) < 0;  // a row of zeros
+        const float w = P.entryWeight ? P.entryWeight[ent] : 1.0f;
+#pragma unroll
+        for (int p = 0; p < FN / 2; ++p) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = acc[2 * p + (i >> 2)][j][i & 3];
+                if (none) v[i] = 0.0f;
+                if (P.entryWeight) v[i] *= w;
+            }
+            const int32_t n = T.n0 + wn + p * 32 + kb * 8;
+            const int64_t o = (int64_t)ent * P.N + n;
+            if (OUT32) {
+                float *out = static_cast<float *>(P.out) + o;
+                if (n < P.N) *reinterpret_cast<f32x4 *>(out) = f32x4{v[0], v[1], v[2], v[3]};
+                if (n + 4 < P.N) *reinterpret_cast<f32x4 *>(out + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            } else if (n < P.N) {
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.out) + o) =
+                    u32x4{bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16,
+                          bf16_rne(v[4]) | bf16_rne(v[5]) << 16, bf16_rne(v[6]) | bf16_rne(v[7]) << 16};
+            }
+        }
+    }
+}
+
+template <int BM, int BN, bool WIDE>
+hipError_t launch_tiles(const ProductParams &P, bool out32, hipStream_t stream) {
+    // row tiles at most: one partly filled for each expert
+    const int64_t tiles = ((int64_t)P.maxEntries / BM + (P.E < P.maxEntries ? P.E : P.maxEntries)) * ceil_div(P.N, BN);
+    const int64_t blocks = (tiles + 7) / 8 * 8;
+    if (blocks > (1 << 23)) return hipErrorInvalidConfiguration;
+    const dim3 grid((uint32_t)blocks);
+    if (out32)
+        hipLaunchKernelGGL((product_tile_kernel<BM, BN, true, WIDE>), grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL((product_tile_kernel<BM, BN, false, WIDE>), grid, dim3(256), 0, stream, P);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_product(const ProductParams &P, bool out32, hipStream_t stream) {
     if (P.maxEntries == 0) return hipSuccess;
+    const int32_t mean = ceil_div(P.maxEntries, P.E);
+    const bool wide = (int64_t)P.numRows * P.rowBytes > 0xf0000000ll;
+    if (mean > 32 && wide) return launch_tiles<128, 128, true>(P, out32, stream);
+    if (mean > 192) return launch_tiles<256, 256, false>(P, out32, stream);
+    if (mean > 32) return launch_tiles<128, 128, false>(P, out32, stream);
     const int32_t per = ceil_div(P.maxEntries, 32 * P.E);
     const dim3 grid((uint32_t)ceil_div(P.N, 64), (uint32_t)(per < 1024 ? per : 1024), (uint32_t)P.E);
     if (out32)

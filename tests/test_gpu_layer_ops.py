@@ -464,6 +464,14 @@ def test_expert_product(sizes, N, H, R, weighted, out):
     check_product(sizes, N, H, out, R, weighted, extra=3)
 
 
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("steps", range(1, 12))
+@pytest.mark.parametrize("tail", [0, 32, 128, 224])
+def test_expert_product_every_number_of_steps(steps, tail, rows):
+    """Rows of 1 to 11 steps of 256 elements, whole or ending inside the last."""
+    check_product([rows, rows + 7], 136, 256 * steps - tail, "fp32", R=97, weighted=True, seed=steps)
+
+
 def test_expert_product_rows_outside_and_odd_offsets():
     rows = np.array([0, -1, 5, 1000000, 3, -2 ** 31, 2 ** 31 - 1, 9] * 10, dtype=np.int32)
     check_product([30, 50], 64, 256, "fp32", R=10, rows=rows, weighted=True)
