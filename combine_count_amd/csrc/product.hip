@@ -14,6 +14,8 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kFp4 = 4;  // the instruction's operand format
 
@@ -37,6 +39,11 @@ __device__ __forceinline__ void mfma_fp4_inplace(f32x4 &c, u32x4 a, u32x4 b, int
                  : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
 }
 __device__ __forceinline__ void mfma_done() { asm volatile("s_nop 15\n\ts_nop 15"); }
+
+// Two values as bf16, the first low, rounded to nearest even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
 
 template <int I>
 struct Const {
@@ -131,54 +138,64 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base)
 }
 
 // What goes between the products of a half besides the reads of the next.
-constexpr int kRequest = 1, kScales = 2;
+constexpr int kRequest = 1, kTurn = 2;
 
 // Where a block's tile lies: expert, entries [m0, hi), columns from n0.
 struct TileAt {
     int32_t e, m0, hi, n0;
 };
 
-// Tile of block b among all experts' tiles (BM entries x BN columns), or
-// e = -1 when there are fewer.  Each XCD (b % 8) takes a contiguous stretch of
-// the tiles, so the tiles that run on it together share operands in its L2;
-// within an expert, up to four row tiles go through the columns together.
-template <int BM, int BN>
-__device__ __forceinline__ TileAt find_tile(const ProductParams &P, int32_t b) {
-    const int lane = threadIdx.x & 63;
-    const int32_t NT = ceil_div(P.N, BN);
+// The groups as a wave holds them, 64 experts at a time (experts e0 + lane):
+// entries [lo, hi) and the row tiles up to and with the lane's expert.
+struct Groups {
+    int32_t lo, hi, incl;
+    int64_t total;  // tiles of all experts
+};
+
+template <int BM>
+__device__ __forceinline__ void load_groups(const ProductParams &P, int32_t e0, Groups &g) {
+    g.lo = g.hi = 0;
+    if (e0 + (int)(threadIdx.x & 63) < P.E) group_range(P, e0 + (threadIdx.x & 63), g.lo, g.hi);
+    g.incl = wave_incl_scan((g.hi - g.lo + BM - 1) / BM);
+}
+
+template <int BM>
+__device__ __forceinline__ Groups count_tiles(const ProductParams &P, int32_t NT) {
+    Groups g;
     int64_t total = 0;
     for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
-        int32_t lo = 0, hi = 0;
-        if (e0 + lane < P.E) group_range(P, e0 + lane, lo, hi);
-        total += __shfl(wave_incl_scan((hi - lo + BM - 1) / BM), 63);
+        load_groups<BM>(P, e0, g);
+        total += uniform(__shfl(g.incl, 63));
     }
-    total *= NT;
-    const int64_t per = (total + 7) / 8;
+    g.total = total * NT;
+    return g;
+}
+
+// Tile b among all experts' tiles (BM entries x BN columns), or e = -1 when
+// there are fewer.  Each XCD (block b % 8) takes a contiguous stretch of the
+// tiles, so the tiles that run on it together share operands in its L2;
+// within an expert, up to four row tiles go through the columns together.
+template <int BM, int BN>
+__device__ __forceinline__ TileAt find_tile(const ProductParams &P, Groups &g, int32_t NT, int32_t b) {
+    const int64_t per = (g.total + 7) / 8;
     const int64_t at = (b & 7) * per + (b >> 3);
-    TileAt t;
-    t.e = -1;
-    if ((b >> 3) >= per || at >= total) return t;
+    TileAt t{-1, 0, 0, 0};
+    if ((b >> 3) >= per || at >= g.total) return t;
     int64_t before = 0;
     for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
-        int32_t lo = 0, hi = 0;
-        if (e0 + lane < P.E) group_range(P, e0 + lane, lo, hi);
-        const int32_t mt = (hi - lo + BM - 1) / BM;
-        const int32_t incl = wave_incl_scan(mt);
-        const uint64_t past = __ballot((before + incl) * NT > at);
+        if (P.E > 64) load_groups<BM>(P, e0, g);
+        const uint64_t past = __ballot((before + g.incl) * NT > at);
         if (past) {
             const int f = __builtin_ctzll(past);
-            const int32_t tiles = __shfl(mt, f);
-            int32_t r = (int32_t)(at - (before + __shfl(incl, f) - tiles) * NT);  // tile inside the expert
-            const int32_t band = r / (4 * NT), rows = min(4, tiles - band * 4);
-            r -= band * 4 * NT;
+            const int32_t lo = __builtin_amdgcn_readlane(g.lo, f), hi = __builtin_amdgcn_readlane(g.hi, f);
+            const int32_t tiles = (hi - lo + BM - 1) / BM;
+            const int32_t r0 = (int32_t)(at - (before + __builtin_amdgcn_readlane(g.incl, f) - tiles) * NT);  // inside the expert
+            const int32_t band = r0 / (4 * NT), rows = min(4, tiles - band * 4), r = r0 - band * 4 * NT;
             const int32_t n = r / rows, m = band * 4 + r - n * rows;
-            t.e = e0 + f;
-            t.m0 = __shfl(lo, f) + m * BM;
-            t.hi = min(__shfl(hi, f), t.m0 + BM);
-            t.n0 = n * BN;
+            t = TileAt{uniform(e0 + f), uniform(lo + m * BM), uniform(min(hi, lo + m * BM + BM)), uniform(n * BN)};
             return t;
         }
-        before += __shfl(incl, 63);
+        before += uniform(__shfl(g.incl, 63));
     }
     return t;
 }
@@ -198,73 +215,105 @@ __device__ __forceinline__ TileAt find_tile(const ProductParams &P, int32_t b) {
 // LDS rows are 128 bytes: the 16-byte pieces of a row are stored at piece ^
 // (row's place among eight), so that the 16 lanes that read one piece of 16
 // rows spread over all banks.
-// Scale bytes: 4 words a row cover two steps; they go through registers into
-// a small LDS array, from which a lane reads the one byte its product needs.
+// Scale bytes: a thread takes one word (128 elements of a row) of the four rows
+// that sit at its place in four fragments, and turns the 4 x 4 bytes over, so
+// that a lane finds the bytes of four fragments in one word of LDS; which of
+// the four a product takes is part of the instruction.  4 words a row cover
+// two steps, so this happens every other step.
+// A block goes on to its next tile (a stride of the grid further) by itself:
+// the first steps of that are requested before this one's results are stored.
 //
 // WIDE: the array of rows passes 32-bit offsets.
 template <int BM, int BN, bool OUT32, bool WIDE>
 __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_kernel(ProductParams P) {
     constexpr int FM = BM / 32, FN = BN / 32;      // 16-wide fragments of a wave
     constexpr int LM = BM / 32, LN = BN / 32;      // LDS loads of a wave per step (8 rows each)
-    constexpr int SR = (BM + BN) / 256;            // scale rows staged per thread
+    constexpr int kQuads = (BM + BN) / 64;         // four fragments each, the rows' first
+    constexpr int SQ = kQuads / 4;                 // of which a wave stages the scales
     __shared__ __attribute__((aligned(16))) uint8_t mbuf0[BM * 128], mbuf1[BM * 128], nbuf0[BN * 128], nbuf1[BN * 128];
-    // scale bytes [step pair][word][byte][fragments by four][row in the fragment][fragment of the four]
-    constexpr int kQuads = (BM + BN) / 64;
-    __shared__ __attribute__((aligned(16))) uint8_t sc[2][4][4][kQuads][16][4];
-    TileAt T = find_tile<BM, BN>(P, blockIdx.x);
-    if (uniform(T.e) < 0) return;
-    T = TileAt{uniform(T.e), uniform(T.m0), uniform(T.hi), uniform(T.n0)};  // so that the compiler knows
+    // scale bytes [step pair][word][byte][quad][row in the fragment][fragment of the four]
+    __shared__ __attribute__((aligned(16))) uint32_t sc[2][4][4][kQuads][16];
+    __shared__ float factor[2][BM];  // the entries' weights, kNoRow for an entry of no row
+    constexpr uint32_t kNoRow = 0x7fdeadedu;
+    const int32_t NT = ceil_div(P.N, BN);
+    Groups groups = count_tiles<BM>(P, NT);
+    int32_t b = blockIdx.x;
+    TileAt T = find_tile<BM, BN>(P, groups, NT, b);
+    if (T.e < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int r16 = lane & 15, kb = lane >> 4;
     const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
 
-    // Row of entry m0 + i, -1 where it is none of the array's; entries behind the tile's last repeat it.
-    auto row_of = [&](int32_t i) -> int32_t {
-        const int32_t ent = min(T.m0 + i, T.hi - 1);
+    // Row of entry m0 + i of a tile, -1 where it is none of the array's; entries behind the tile's last repeat it.
+    auto row_of = [&](const TileAt &t, int32_t i) -> int32_t {
+        const int32_t ent = min(t.m0 + i, t.hi - 1);
         const int32_t r = P.entryRow ? P.entryRow[ent] : ent;
         return (uint32_t)r < (uint32_t)P.numRows ? r : -1;
     };
     const int piece_m = ((lane & 7) ^ (lane >> 3)) * 16;
     const int piece_n0 = ((lane & 7) ^ ((lane >> 3) & 3)) * 16, piece_n1 = piece_n0 ^ 64;
     // Offsets of what this lane requests in a step: of the rows (their index where offsets pass 32 bits), and of the
-    // columns from the tile's first.
-    uint32_t mat[LM], nat[LN];
-    const uint8_t *nbase = P.weights + ((int64_t)T.e * P.N + T.n0) * P.rowBytes;
-    const __amdgpu_buffer_rsrc_t mrs = buffer_of(P.rows), nrs = buffer_of(nbase);
+    // columns from the tile's first; and those of the scale words it stages.
+    uint32_t mat[LM], nat[LN], sat[SQ][4];
+    const int sword = lane & 3, sslot = lane >> 2;  // the word and the row in its fragment that it stages
+    const uint8_t *nbase, *nsbase;
+    auto set_tile = [&](const TileAt &t, int par) {
+        int ln = lane;  // opaque: what follows is computed here, not kept in registers from tile to tile
+        asm volatile("" : "+v"(ln));
+        const int td = wave * 64 + ln, srow = ln >> 2, place_n0 = ((ln & 7) ^ ((ln >> 3) & 3)) * 16;
+        nbase = P.weights + ((int64_t)t.e * P.N + t.n0) * P.rowBytes;
+        nsbase = P.weightScales + ((int64_t)t.e * P.N + t.n0) * P.words * 4;
 #pragma unroll
-    for (int t = 0; t < LM; ++t) {
-        mat[t] = (uint32_t)max(row_of(wave * (BM / 4) + t * 8 + (lane >> 3)), 0);
-        if (!WIDE) mat[t] = mat[t] * (uint32_t)P.rowBytes + piece_m;
-    }
+        for (int i = 0; i < LM; ++i) mat[i] = (uint32_t)row_of(t, wave * (BM / 4) + i * 8 + (ln >> 3));
 #pragma unroll
-    for (int t = 0; t < LN; ++t)
-        nat[t] = (uint32_t)(min(wave * (BN / 4) + t * 8 + (lane >> 3), P.N - 1 - T.n0) * P.rowBytes) + (t & 1 ? piece_n1 : piece_n0);
-    const uint8_t *sptr[SR];  // scale rows this thread stages: rows of the tile first, then columns
+        for (int q = 0; q < SQ; ++q) {
+            const int quad = q * 4 + wave;
 #pragma unroll
-    for (int t = 0; t < SR; ++t) {
-        const int i = t * 256 + tid;
-        const uint8_t *m = P.rowScales + (int64_t)max(row_of(min(i, BM - 1)), 0) * P.words * 4;
-        const uint8_t *n = P.weightScales + ((int64_t)T.e * P.N + min(T.n0 + max(i - BM, 0), P.N - 1)) * P.words * 4;
-        sptr[t] = i < BM ? m : n;
-    }
+            for (int f = 0; f < 4; ++f) {
+                if (quad < BM / 64) {
+                    sat[q][f] = (uint32_t)max(row_of(t, quad * 64 + f * 16 + srow), 0);
+                } else {
+                    const int n = (quad - BM / 64) * 64 + (f >> 1) * 32 + (srow >> 2) * 8 + (f & 1) * 4 + (srow & 3);
+                    sat[q][f] = (uint32_t)min(n, P.N - 1 - t.n0);
+                }
+                if (!WIDE) sat[q][f] *= (uint32_t)P.words * 4;
+            }
+        }
+        if (td < BM) {
+            const float w = P.entryWeight ? P.entryWeight[min(t.m0 + td, t.hi - 1)] : 1.0f;
+            factor[par][td] = row_of(t, td) < 0 ? __uint_as_float(kNoRow) : w;
+        }
+#pragma unroll
+        for (int i = 0; i < LM; ++i) {
+            mat[i] = (uint32_t)max((int32_t)mat[i], 0);
+            if (!WIDE) mat[i] = mat[i] * (uint32_t)P.rowBytes + ((ln & 7) ^ (ln >> 3)) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < LN; ++i)
+            nat[i] = (uint32_t)(min(wave * (BN / 4) + i * 8 + (ln >> 3), P.N - 1 - t.n0) * P.rowBytes) + (i & 1 ? place_n0 ^ 64 : place_n0);
+    };
+    const __amdgpu_buffer_rsrc_t mrs = buffer_of(P.rows);
     const int NK = (P.rowBytes + 127) / 128, blocks = P.H / 32;
     const int tail = NK * 128 - P.rowBytes;  // bytes of the last step behind the rows' end
 
     // Load t of the wave's LM + LN in step k.  Pieces behind the end of the rows repeat the last one (clear_tail).
-    auto request = [&](auto t, int k, uint8_t *mb, uint8_t *nb) {
+    auto request = [&](auto t, int step, uint8_t *mb, uint8_t *nb) {
+        const int k = uniform(step);
         constexpr int I = decltype(t)::value;
+        int w = wave;  // opaque: the place is added up here, not kept in 16 scalar registers
+        asm volatile("" : "+s"(w));
         if constexpr (I < LM) {
-            uint8_t *to = mb + (wave * (BM / 4) + I * 8) * 128;
+            uint8_t *to = mb + (w * (BM / 4) + I * 8) * 128;
             if constexpr (WIDE)
                 load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(k * 128 + piece_m)), to);
             else
                 load_lds16(mrs, mat[I], k * 128, to);
         } else {
-            load_lds16(nrs, nat[I - LM], k * 128, nb + (wave * (BN / 4) + (I - LM) * 8) * 128);
+            load_lds16(buffer_of(nbase), nat[I - LM], k * 128, nb + (w * (BN / 4) + (I - LM) * 8) * 128);
         }
     };
     auto request_last = [&](uint8_t *mb, uint8_t *nb) {  // step NK - 1, which the rows may end in
-        const int at = (NK - 1) * 128, last = 112 - tail;  // the last piece there is
+        const int at = uniform((NK - 1) * 128), last = 112 - tail;  // the last piece there is
         each<LM>([&](auto t) {
             constexpr int I = decltype(t)::value;
             uint8_t *to = mb + (wave * (BM / 4) + I * 8) * 128;
@@ -277,7 +326,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         each<LN>([&](auto t) {
             constexpr int I = decltype(t)::value;
             const int own = I & 1 ? piece_n1 : piece_n0;
-            load_lds16(nrs, nat[I] - own + min(own, last), at, nb + (wave * (BN / 4) + I * 8) * 128);
+            load_lds16(buffer_of(nbase), nat[I] - own + min(own, last), at, nb + (wave * (BN / 4) + I * 8) * 128);
         });
     };
     // Rows that end inside the last step: zeros in the entries' pieces behind the end, once they have arrived.
@@ -290,31 +339,34 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
                 *reinterpret_cast<u32x4 *>(mb + wave * (BM / 4) * 128 + t * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
         __syncthreads();
     };
-    u32x4 sreg[SR];
-    auto scales_load = [&](int pair) {  // words 4 pair .. + 3 of the staged rows; 127 behind the row's last block
-        if (pair * 16 + 16 <= blocks) {
+    uint32_t sreg[SQ][4];
+    auto scales_load = [&](int pair) {  // words 4 pair .. + 3, behind the rows' end the last one again
+        const uint32_t at = (uint32_t)min(pair * 4 + sword, P.words - 1) * 4;
 #pragma unroll
-            for (int t = 0; t < SR; ++t) sreg[t] = *reinterpret_cast<const u32x4_dword *>(sptr[t] + pair * 16);
-        } else {
+        for (int q = 0; q < SQ; ++q) {
+            const uint8_t *base = q * 4 + wave < BM / 64 ? P.rowScales : nsbase;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int left = blocks - pair * 16 - w * 4;  // blocks of this word
-                const uint32_t keep = left >= 4 ? 0xffffffffu : left > 0 ? (1u << (left * 8)) - 1 : 0u;
-#pragma unroll
-                for (int t = 0; t < SR; ++t) {
-                    const uint32_t v = *reinterpret_cast<const uint32_t *>(sptr[t] + min(pair * 4 + w, P.words - 1) * 4);
-                    sreg[t][w] = (v & keep) | (0x7f7f7f7fu & ~keep);
-                }
+            for (int f = 0; f < 4; ++f) {
+                if constexpr (WIDE)
+                    sreg[q][f] = *reinterpret_cast<const uint32_t *>(base + ((uint64_t)sat[q][f] * ((uint32_t)P.words * 4) + at));
+                else
+                    sreg[q][f] = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(base), (int)(sat[q][f] + at), 0, 0);
             }
         }
     };
-    auto scale_store = [&](auto j, int pair) {  // one of the 16 SR bytes this thread stages for a pair of steps
-        constexpr int t = decltype(j)::value / 16, w = decltype(j)::value / 4 % 4, b = decltype(j)::value % 4;
-        const int i = t * 256 + tid, n = i - BM;
-        const int quad = i < BM ? i >> 6 : BM / 64 + (n >> 6);
-        const int r = i < BM ? i & 15 : ((n >> 3) & 3) * 4 + (n & 3);
-        const int f = i < BM ? (i >> 4) & 3 : ((n >> 5) & 1) * 2 + ((n >> 2) & 1);
-        sc[pair & 1][w][b][quad][r][f] = (uint8_t)(sreg[t][w] >> (8 * b));
+    auto scales_arrived = [&](int pair) {  // 127 behind the rows' last block
+        const int left = blocks - (pair * 4 + sword) * 4;  // blocks of this word
+        const uint32_t keep = left >= 4 ? 0xffffffffu : left > 0 ? (1u << (left * 8)) - 1 : 0u;
+#pragma unroll
+        for (int q = 0; q < SQ; ++q)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) sreg[q][f] = (sreg[q][f] & keep) | (0x7f7f7f7fu & ~keep);
+    };
+    auto scale_store = [&](auto j, int pair) {  // byte b of the four rows' words: one of the 4 SQ words this thread stages
+        constexpr int q = decltype(j)::value / 4, b = decltype(j)::value % 4;
+        const uint32_t lo = __builtin_amdgcn_perm(sreg[q][1], sreg[q][0], (uint32_t)(b | (b + 4) << 8 | 0x0c0c0000));
+        const uint32_t hi = __builtin_amdgcn_perm(sreg[q][3], sreg[q][2], (uint32_t)(b << 16 | (b + 4) << 24 | 0x0c0c));
+        sc[pair & 1][sword][b][q * 4 + wave][sslot] = lo | hi;
     };
 
     struct Half {
@@ -330,11 +382,11 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     auto read_scales = [&](Scales &s, int k) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint8_t(*sp)[16][4] = sc[(k >> 1) & 1][(k & 1) * 2 + half][kb];
+            const uint32_t(*sp)[16] = sc[(k >> 1) & 1][(k & 1) * 2 + half][kb];
 #pragma unroll
-            for (int q = 0; q < FN / 4; ++q) s.n[half][q] = *reinterpret_cast<const int32_t *>(sp[(BM + wn) / 64 + q][r16]);
+            for (int q = 0; q < FN / 4; ++q) s.n[half][q] = (int32_t)sp[(BM + wn) / 64 + q][r16];
 #pragma unroll
-            for (int q = 0; q < FM / 4; ++q) s.m[half][q] = *reinterpret_cast<const int32_t *>(sp[wm / 64 + q][r16]);
+            for (int q = 0; q < FM / 4; ++q) s.m[half][q] = (int32_t)sp[wm / 64 + q][r16];
         }
     };
     constexpr int kReads = FM + FN;
@@ -351,17 +403,10 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         }
     };
     f32x4 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            acc[i][j] = f32x4{0, 0, 0, 0};
-            asm volatile("" : "+a"(acc[i][j]));
-        }
-    mfma_done();
     // The products of half HALF of a step, one matrix instruction after the other; dealt out between them, where the
     // matrix instructions leave issue slots: the reads of the next half from mb and nb, and, by WITH, the requests of
-    // step rk into rmb and rnb or the scales of step pair rk into LDS.
+    // step rk into rmb and rnb, where rk begins a pair of steps after its scales have gone into LDS and the next pair's
+    // have been asked for.
     auto multiply = [&](auto half, auto with, const Half &h, const Scales &s, Half &next, const uint8_t *mb, const uint8_t *nb,
                         int rk, uint8_t *rmb, uint8_t *rnb) {
         constexpr int HALF = decltype(half)::value, WITH = decltype(with)::value, kAll = FM * FN;
@@ -370,14 +415,15 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
             mfma_fp4_inplace<I & 3, J & 3>(acc[I][J], h.n[I], h.m[J], s.n[HALF][I >> 2], s.m[HALF][J >> 2]);
             constexpr int kGap = kAll / (kReads + 1) ? kAll / (kReads + 1) : 1;
             if constexpr (Q % kGap == 0 && Q / kGap < kReads) read(Const<Q / kGap>{}, next, mb, nb, 1 - HALF);
-            if constexpr (WITH == kRequest) {
-                constexpr int kReqGap = kAll / (LM + LN);
-                if constexpr (Q % kReqGap == kReqGap / 2) request(Const<Q / kReqGap>{}, rk, rmb, rnb);
-            }
-            if constexpr (WITH == kScales && Q >= kAll * 3 / 4) {
-                constexpr int kPer = 16 * SR / (kAll / 4);
-                each<kPer>([&](auto i) { scale_store(Const<(Q - kAll * 3 / 4) * kPer + decltype(i)::value>{}, rk); });
-            }
+            // requests after the stores of the scales: those would wait for requests under way (to other parts of LDS,
+            // which the compiler does not tell apart)
+            constexpr int kFrom = WITH == kTurn ? kAll / 4 : 0, kReqGap = (kAll - kFrom) / (LM + LN);
+            if constexpr (WITH == kTurn && Q == 0) scales_arrived(rk >> 1);
+            if constexpr (WITH == kTurn && Q < kFrom && Q % (kFrom / (4 * SQ)) == 0)
+                scale_store(Const<Q / (kFrom / (4 * SQ))>{}, rk >> 1);
+            if constexpr (WITH == kTurn && Q == kFrom - 1) scales_load((rk >> 1) + 1);
+            if constexpr (WITH != 0 && Q >= kFrom && (Q - kFrom) % kReqGap == kReqGap / 2 && (Q - kFrom) / kReqGap < LM + LN)
+                request(Const<(Q - kFrom) / kReqGap>{}, rk, rmb, rnb);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
@@ -385,7 +431,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     using Second = Const<1>;
     using Alone = Const<0>;
     using Request = Const<kRequest>;
-    using ScaleStore = Const<kScales>;
+    using Turn = Const<kTurn>;
     auto meet = [&] {  // this wave's LDS reads are in its registers, its requests have arrived; then all waves' have
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
@@ -395,18 +441,32 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
 
     Half h0, h1;
     Scales s0, s1;  // of even and odd steps
-    scales_load(0);
-    each<16 * SR>([&](auto j) { scale_store(j, 0); });
-    if (NK == 1) {
-        request_last(mbuf0, nbuf0);
-    } else {
-        each<LM + LN>([&](auto t) { request(t, 0, mbuf0, nbuf0); });
-        if (NK == 2)
-            request_last(mbuf1, nbuf1);
-        else
-            each<LM + LN>([&](auto t) { request(t, 1, mbuf1, nbuf1); });
-    }
+    auto request_first = [&] {  // the tile's first two steps and their scales
+        scales_load(0);
+        if (NK == 1) {
+            request_last(mbuf0, nbuf0);
+        } else {
+            each<LM + LN>([&](auto t) { request(t, 0, mbuf0, nbuf0); });
+            if (NK == 2)
+                request_last(mbuf1, nbuf1);
+            else
+                each<LM + LN>([&](auto t) { request(t, 1, mbuf1, nbuf1); });
+        }
+    };
+    set_tile(T, 0);
+    request_first();
+    for (int par = 0;; par ^= 1) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            acc[i][j] = f32x4{0, 0, 0, 0};
+            asm volatile("" : "+a"(acc[i][j]));
+        }
+    scales_arrived(0);
+    each<4 * SQ>([&](auto j) { scale_store(j, 0); });
     meet();
+    scales_load(1);
     if (NK == 1) clear_tail(mbuf0);
     read_scales(s0, 0);
     each<kReads>([&](auto r) { read(r, h0, mbuf0, nbuf0, 0); });
@@ -415,9 +475,8 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         multiply(First{}, Alone{}, h0, s0, h1, mbuf0, nbuf0, 0, mbuf0, nbuf0);
         meet();
         read_scales(s1, k + 1);
-        scales_load((k >> 1) + 1);
-        multiply(Second{}, Request{}, h1, s0, h0, mbuf1, nbuf1, k + 2, mbuf0, nbuf0);
-        multiply(First{}, ScaleStore{}, h0, s1, h1, mbuf1, nbuf1, (k >> 1) + 1, mbuf0, nbuf0);
+        multiply(Second{}, Turn{}, h1, s0, h0, mbuf1, nbuf1, k + 2, mbuf0, nbuf0);
+        multiply(First{}, Alone{}, h0, s1, h1, mbuf1, nbuf1, 0, mbuf0, nbuf0);
         meet();
         read_scales(s0, k + 2);
         multiply(Second{}, Request{}, h1, s1, h0, mbuf0, nbuf0, k + 3, mbuf1, nbuf1);
@@ -429,7 +488,9 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         if (k + 2 == NK) clear_tail(mbuf1);
         read_scales(s1, k + 1);
         if (k + 2 < NK) {
-            scales_load((k >> 1) + 1);
+            scales_arrived((k >> 1) + 1);
+            each<4 * SQ>([&](auto j) { scale_store(j, (k >> 1) + 1); });
+            scales_load((k >> 1) + 2);
             if (k + 3 == NK)
                 request_last(mbuf0, nbuf0);
             else
@@ -437,7 +498,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         }
         multiply(Second{}, Alone{}, h1, s0, h0, mbuf1, nbuf1, 0, mbuf0, nbuf0);
         if (k + 1 >= NK) break;
-        multiply(First{}, ScaleStore{}, h0, s1, h1, mbuf1, nbuf1, (k >> 1) + 1, mbuf0, nbuf0);
+        multiply(First{}, Alone{}, h0, s1, h1, mbuf1, nbuf1, 0, mbuf0, nbuf0);
         meet();
         if (k + 3 == NK) clear_tail(mbuf0);
         read_scales(s0, k + 2);
@@ -447,22 +508,26 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     }
     mfma_done();
 
+    // No wave needs this tile's LDS any more (all passed the last meeting): the next tile's first steps.
+    const TileAt done = T;
+    b += gridDim.x;
+    T = find_tile<BM, BN>(P, groups, NT, b);
+    if (T.e >= 0) {
+        set_tile(T, par ^ 1);
+        request_first();
+    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-        const int32_t ent = T.m0 + mrow + j * 16;
-        if (ent >= T.hi) continue;
-        const bool none = row_of(mrow + j * 16) < 0;  // a row of zeros
-        const float w = P.entryWeight ? P.entryWeight[ent] : 1.0f;
+        const int32_t ent = done.m0 + mrow + j * 16;
+        if (ent >= done.hi) continue;
+        const float w = factor[par][mrow + j * 16];
+        const bool none = __float_as_uint(w) == kNoRow;
 #pragma unroll
         for (int p = 0; p < FN / 2; ++p) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = acc[2 * p + (i >> 2)][j][i & 3];
-                if (none) v[i] = 0.0f;
-                if (P.entryWeight) v[i] *= w;
-            }
-            const int32_t n = T.n0 + wn + p * 32 + kb * 8;
+            for (int i = 0; i < 8; ++i) v[i] = none ? 0.0f : acc[2 * p + (i >> 2)][j][i & 3] * w;
+            const int32_t n = done.n0 + wn + p * 32 + kb * 8;
             const int64_t o = (int64_t)ent * P.N + n;
             if (OUT32) {
                 float *out = static_cast<float *>(P.out) + o;
@@ -470,10 +535,11 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
                 if (n + 4 < P.N) *reinterpret_cast<f32x4 *>(out + 4) = f32x4{v[4], v[5], v[6], v[7]};
             } else if (n < P.N) {
                 *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.out) + o) =
-                    u32x4{bf16_rne(v[0]) | bf16_rne(v[1]) << 16, bf16_rne(v[2]) | bf16_rne(v[3]) << 16,
-                          bf16_rne(v[4]) | bf16_rne(v[5]) << 16, bf16_rne(v[6]) | bf16_rne(v[7]) << 16};
+                    u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
             }
         }
+    }
+    if (T.e < 0) return;
     }
 }
 
@@ -481,9 +547,14 @@ template <int BM, int BN, bool WIDE>
 hipError_t launch_tiles(const ProductParams &P, bool out32, hipStream_t stream) {
     // row tiles at most: one partly filled for each expert
     const int64_t tiles = ((int64_t)P.maxEntries / BM + (P.E < P.maxEntries ? P.E : P.maxEntries)) * ceil_div(P.N, BN);
-    const int64_t blocks = (tiles + 7) / 8 * 8;
-    if (blocks > (1 << 23)) return hipErrorInvalidConfiguration;
-    const dim3 grid((uint32_t)blocks);
+    if (tiles > INT32_MAX / 2) return hipErrorInvalidConfiguration;
+    int device = 0, cus = 0;
+    hipError_t err = hipGetDevice(&device);
+    if (err == hipSuccess) err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    if (err != hipSuccess) return err;
+    // as many blocks as run at once, a multiple of the 8 XCDs
+    const int64_t most = (int64_t)ceil_div(cus * (BM * BN > 128 * 128 ? 1 : 2), 8) * 8, blocks = (tiles + 7) / 8 * 8;
+    const dim3 grid((uint32_t)(blocks < most ? blocks : most));
     if (out32)
         hipLaunchKernelGGL((product_tile_kernel<BM, BN, true, WIDE>), grid, dim3(256), 0, stream, P);
     else
