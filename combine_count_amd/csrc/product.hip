@@ -233,45 +233,66 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     __shared__ __attribute__((aligned(16))) uint8_t mbuf0[BM * 128], mbuf1[BM * 128], nbuf0[BN * 128], nbuf1[BN * 128];
     // scale bytes [step pair][word][byte][quad][row in the fragment][fragment of the four]
     __shared__ __attribute__((aligned(16))) uint32_t sc[2][4][4][kQuads][16];
-    __shared__ float factor[2][BM];  // the entries' weights, kNoRow for an entry of no row
-    constexpr uint32_t kNoRow = 0x7fdeadedu;
+    // of this and the next tile: the entries' rows (-1: none of the array's) and weights
+    __shared__ int32_t rows[2][BM];
+    __shared__ float factor[2][BM];
     const int32_t NT = ceil_div(P.N, BN);
     Groups groups = count_tiles<BM>(P, NT);
     int32_t b = blockIdx.x;
     TileAt T = find_tile<BM, BN>(P, groups, NT, b);
     if (T.e < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int r16 = lane & 15, kb = lane >> 4;
     const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
 
-    // Row of entry m0 + i of a tile, -1 where it is none of the array's; entries behind the tile's last repeat it.
-    auto row_of = [&](const TileAt &t, int32_t i) -> int32_t {
-        const int32_t ent = min(t.m0 + i, t.hi - 1);
-        const int32_t r = P.entryRow ? P.entryRow[ent] : ent;
-        return (uint32_t)r < (uint32_t)P.numRows ? r : -1;
+    // The lane again, opaque: what is computed from it is computed there, not kept in registers from tile to tile.
+    auto fresh = [&] {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return l;
     };
-    const int piece_m = ((lane & 7) ^ (lane >> 3)) * 16;
-    const int piece_n0 = ((lane & 7) ^ ((lane >> 3) & 3)) * 16, piece_n1 = piece_n0 ^ 64;
+    // A tile's rows and weights, on the way to LDS.  Entries behind the tile's last repeat it.
+    int32_t row = -1;
+    float weight = 1.0f;
+    auto look = [&](const TileAt &t) {
+        const int tid = wave * 64 + fresh();
+        if (tid >= BM) return;
+        const int32_t ent = min(t.m0 + tid, t.hi - 1);
+        row = P.entryRow ? P.entryRow[ent] : ent;
+        if (P.entryWeight) weight = P.entryWeight[ent];
+    };
+    auto keep = [&](int par) {
+        const int tid = wave * 64 + fresh();
+        if (tid >= BM) return;
+        rows[par][tid] = (uint32_t)row < (uint32_t)P.numRows ? row : -1;
+        factor[par][tid] = weight;
+    };
+    // The 16-byte piece of a row that lane l requests: of the tile's rows, and of its columns in even loads (in odd
+    // ones ^ 64).
+    auto piece_m = [](int l) { return ((l & 7) ^ (l >> 3)) * 16; };
+    auto piece_n = [](int l) { return ((l & 7) ^ ((l >> 3) & 3)) * 16; };
     // Offsets of what this lane requests in a step: of the rows (their index where offsets pass 32 bits), and of the
     // columns from the tile's first; and those of the scale words it stages.
     uint32_t mat[LM], nat[LN], sat[SQ][4];
     const int sword = lane & 3, sslot = lane >> 2;  // the word and the row in its fragment that it stages
     const uint8_t *nbase, *nsbase;
     auto set_tile = [&](const TileAt &t, int par) {
-        int ln = lane;  // opaque: what follows is computed here, not kept in registers from tile to tile
-        asm volatile("" : "+v"(ln));
-        const int td = wave * 64 + ln, srow = ln >> 2, place_n0 = ((ln & 7) ^ ((ln >> 3) & 3)) * 16;
+        const int ln = fresh();
+        const int srow = ln >> 2;
         nbase = P.weights + ((int64_t)t.e * P.N + t.n0) * P.rowBytes;
         nsbase = P.weightScales + ((int64_t)t.e * P.N + t.n0) * P.words * 4;
 #pragma unroll
-        for (int i = 0; i < LM; ++i) mat[i] = (uint32_t)row_of(t, wave * (BM / 4) + i * 8 + (ln >> 3));
+        for (int i = 0; i < LM; ++i) {
+            mat[i] = (uint32_t)max(rows[par][wave * (BM / 4) + i * 8 + (ln >> 3)], 0);
+            if (!WIDE) mat[i] = mat[i] * (uint32_t)P.rowBytes + piece_m(ln);
+        }
 #pragma unroll
         for (int q = 0; q < SQ; ++q) {
             const int quad = q * 4 + wave;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 if (quad < BM / 64) {
-                    sat[q][f] = (uint32_t)max(row_of(t, quad * 64 + f * 16 + srow), 0);
+                    sat[q][f] = (uint32_t)max(rows[par][quad * 64 + f * 16 + srow], 0);
                 } else {
                     const int n = (quad - BM / 64) * 64 + (f >> 1) * 32 + (srow >> 2) * 8 + (f & 1) * 4 + (srow & 3);
                     sat[q][f] = (uint32_t)min(n, P.N - 1 - t.n0);
@@ -279,18 +300,9 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
                 if (!WIDE) sat[q][f] *= (uint32_t)P.words * 4;
             }
         }
-        if (td < BM) {
-            const float w = P.entryWeight ? P.entryWeight[min(t.m0 + td, t.hi - 1)] : 1.0f;
-            factor[par][td] = row_of(t, td) < 0 ? __uint_as_float(kNoRow) : w;
-        }
-#pragma unroll
-        for (int i = 0; i < LM; ++i) {
-            mat[i] = (uint32_t)max((int32_t)mat[i], 0);
-            if (!WIDE) mat[i] = mat[i] * (uint32_t)P.rowBytes + ((ln & 7) ^ (ln >> 3)) * 16;
-        }
 #pragma unroll
         for (int i = 0; i < LN; ++i)
-            nat[i] = (uint32_t)(min(wave * (BN / 4) + i * 8 + (ln >> 3), P.N - 1 - t.n0) * P.rowBytes) + (i & 1 ? place_n0 ^ 64 : place_n0);
+            nat[i] = (uint32_t)(min(wave * (BN / 4) + i * 8 + (ln >> 3), P.N - 1 - t.n0) * P.rowBytes) + (piece_n(ln) ^ (i & 1) * 64);
     };
     const __amdgpu_buffer_rsrc_t mrs = buffer_of(P.rows);
     const int NK = (P.rowBytes + 127) / 128, blocks = P.H / 32;
@@ -305,7 +317,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         if constexpr (I < LM) {
             uint8_t *to = mb + (w * (BM / 4) + I * 8) * 128;
             if constexpr (WIDE)
-                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(k * 128 + piece_m)), to);
+                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(k * 128 + piece_m(lane))), to);
             else
                 load_lds16(mrs, mat[I], k * 128, to);
         } else {
@@ -314,18 +326,18 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     };
     auto request_last = [&](uint8_t *mb, uint8_t *nb) {  // step NK - 1, which the rows may end in
         const int at = uniform((NK - 1) * 128), last = 112 - tail;  // the last piece there is
+        const int ln = fresh(), m = piece_m(ln), n0 = piece_n(ln), n1 = n0 ^ 64;
         each<LM>([&](auto t) {
             constexpr int I = decltype(t)::value;
             uint8_t *to = mb + (wave * (BM / 4) + I * 8) * 128;
-            const int piece = min(piece_m, last);
             if constexpr (WIDE)
-                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(at + piece)), to);
+                load_lds16(P.rows + ((uint64_t)mat[I] * (uint32_t)P.rowBytes + (uint32_t)(at + min(m, last))), to);
             else
-                load_lds16(mrs, mat[I] - piece_m + piece, at, to);
+                load_lds16(mrs, mat[I] - m + min(m, last), at, to);
         });
         each<LN>([&](auto t) {
             constexpr int I = decltype(t)::value;
-            const int own = I & 1 ? piece_n1 : piece_n0;
+            const int own = I & 1 ? n1 : n0;
             load_lds16(buffer_of(nbase), nat[I] - own + min(own, last), at, nb + (wave * (BN / 4) + I * 8) * 128);
         });
     };
@@ -333,14 +345,18 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     // (The weights' pieces there hold finite values and scales: nothing adds up.)
     auto clear_tail = [&](uint8_t *mb) {
         if (tail == 0) return;
+        const int ln = fresh();
 #pragma unroll
         for (int t = 0; t < LM; ++t)
-            if (piece_m >= 128 - tail)
-                *reinterpret_cast<u32x4 *>(mb + wave * (BM / 4) * 128 + t * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+            if (piece_m(ln) >= 128 - tail)
+                *reinterpret_cast<u32x4 *>(mb + wave * (BM / 4) * 128 + t * 1024 + ln * 16) = u32x4{0, 0, 0, 0};
         __syncthreads();
     };
-    uint32_t sreg[SQ][4];
-    auto scales_load = [&](int pair) {  // words 4 pair .. + 3, behind the rows' end the last one again
+    struct Words {
+        uint32_t w[SQ][4];
+    };
+    Words sreg;  // the next pair of steps' scale words, on the way to LDS
+    auto scales_load = [&](Words &sreg, int pair) {  // words 4 pair .. + 3, behind the rows' end the last one again
         const uint32_t at = (uint32_t)min(pair * 4 + sword, P.words - 1) * 4;
 #pragma unroll
         for (int q = 0; q < SQ; ++q) {
@@ -348,24 +364,24 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 if constexpr (WIDE)
-                    sreg[q][f] = *reinterpret_cast<const uint32_t *>(base + ((uint64_t)sat[q][f] * ((uint32_t)P.words * 4) + at));
+                    sreg.w[q][f] = *reinterpret_cast<const uint32_t *>(base + ((uint64_t)sat[q][f] * ((uint32_t)P.words * 4) + at));
                 else
-                    sreg[q][f] = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(base), (int)(sat[q][f] + at), 0, 0);
+                    sreg.w[q][f] = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(base), (int)(sat[q][f] + at), 0, 0);
             }
         }
     };
-    auto scales_arrived = [&](int pair) {  // 127 behind the rows' last block
+    auto scales_arrived = [&](Words &sreg, int pair) {  // 127 behind the rows' last block
         const int left = blocks - (pair * 4 + sword) * 4;  // blocks of this word
         const uint32_t keep = left >= 4 ? 0xffffffffu : left > 0 ? (1u << (left * 8)) - 1 : 0u;
 #pragma unroll
         for (int q = 0; q < SQ; ++q)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) sreg[q][f] = (sreg[q][f] & keep) | (0x7f7f7f7fu & ~keep);
+            for (int f = 0; f < 4; ++f) sreg.w[q][f] = (sreg.w[q][f] & keep) | (0x7f7f7f7fu & ~keep);
     };
-    auto scale_store = [&](auto j, int pair) {  // byte b of the four rows' words: one of the 4 SQ words this thread stages
+    auto scale_store = [&](auto j, const Words &sreg, int pair) {  // byte b of the four rows' words: one of the 4 SQ words this thread stages
         constexpr int q = decltype(j)::value / 4, b = decltype(j)::value % 4;
-        const uint32_t lo = __builtin_amdgcn_perm(sreg[q][1], sreg[q][0], (uint32_t)(b | (b + 4) << 8 | 0x0c0c0000));
-        const uint32_t hi = __builtin_amdgcn_perm(sreg[q][3], sreg[q][2], (uint32_t)(b << 16 | (b + 4) << 24 | 0x0c0c));
+        const uint32_t lo = __builtin_amdgcn_perm(sreg.w[q][1], sreg.w[q][0], (uint32_t)(b | (b + 4) << 8 | 0x0c0c0000));
+        const uint32_t hi = __builtin_amdgcn_perm(sreg.w[q][3], sreg.w[q][2], (uint32_t)(b << 16 | (b + 4) << 24 | 0x0c0c));
         sc[pair & 1][sword][b][q * 4 + wave][sslot] = lo | hi;
     };
 
@@ -418,10 +434,10 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
             // requests after the stores of the scales: those would wait for requests under way (to other parts of LDS,
             // which the compiler does not tell apart)
             constexpr int kFrom = WITH == kTurn ? kAll / 4 : 0, kReqGap = (kAll - kFrom) / (LM + LN);
-            if constexpr (WITH == kTurn && Q == 0) scales_arrived(rk >> 1);
+            if constexpr (WITH == kTurn && Q == 0) scales_arrived(sreg, rk >> 1);
             if constexpr (WITH == kTurn && Q < kFrom && Q % (kFrom / (4 * SQ)) == 0)
-                scale_store(Const<Q / (kFrom / (4 * SQ))>{}, rk >> 1);
-            if constexpr (WITH == kTurn && Q == kFrom - 1) scales_load((rk >> 1) + 1);
+                scale_store(Const<Q / (kFrom / (4 * SQ))>{}, sreg, rk >> 1);
+            if constexpr (WITH == kTurn && Q == kFrom - 1) scales_load(sreg, (rk >> 1) + 1);
             if constexpr (WITH != 0 && Q >= kFrom && (Q - kFrom) % kReqGap == kReqGap / 2 && (Q - kFrom) / kReqGap < LM + LN)
                 request(Const<(Q - kFrom) / kReqGap>{}, rk, rmb, rnb);
             __builtin_amdgcn_sched_barrier(0);
@@ -432,17 +448,22 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     using Alone = Const<0>;
     using Request = Const<kRequest>;
     using Turn = Const<kTurn>;
-    auto meet = [&] {  // this wave's LDS reads are in its registers, its requests have arrived; then all waves' have
+    // This wave's LDS reads are in its registers and all but its last `left` requests (loads, and stores of results)
+    // are done; then all waves' are.
+    auto meet = [&](auto left) {
+        constexpr int L = decltype(left)::value;
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt((L & 15) | (L >> 4) << 14 | 0x70);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    using All = Const<0>;
 
     Half h0, h1;
     Scales s0, s1;  // of even and odd steps
-    auto request_first = [&] {  // the tile's first two steps and their scales
-        scales_load(0);
+    Words sfirst;
+    auto request_first = [&] {  // the tile's first two steps and the scales of its first four
+        scales_load(sfirst, 0);
         if (NK == 1) {
             request_last(mbuf0, nbuf0);
         } else {
@@ -452,45 +473,70 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
             else
                 each<LM + LN>([&](auto t) { request(t, 1, mbuf1, nbuf1); });
         }
+        scales_load(sreg, 1);
     };
+    // Stores of results per wave and tile, whatever the tile holds: they stay under way while the next tile begins.
+    constexpr int kStores = FM * FN / 2 * (OUT32 ? 2 : 1), kStoresLeft = kStores < 63 ? kStores : 63;
+    // A tile's sums begin at zero, its first scales go into LDS.
+    auto begin = [&] {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                acc[i][j] = f32x4{0, 0, 0, 0};
+                asm volatile("" : "+a"(acc[i][j]));
+            }
+        scales_arrived(sfirst, 0);
+        each<4 * SQ>([&](auto j) { scale_store(j, sfirst, 0); });
+    };
+    // For the compiler: the words on the way have arrived here (it would wait for later stores too).
+    auto settle = [&] {
+#pragma unroll
+        for (int q = 0; q < SQ; ++q)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) asm volatile("" : "+v"(sreg.w[q][f]));
+    };
+    look(T);
+    keep(0);
+    meet(All{});
     set_tile(T, 0);
     request_first();
+    begin();
+    meet(All{});
+    settle();
     for (int par = 0;; par ^= 1) {
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            acc[i][j] = f32x4{0, 0, 0, 0};
-            asm volatile("" : "+a"(acc[i][j]));
-        }
-    scales_arrived(0);
-    each<4 * SQ>([&](auto j) { scale_store(j, 0); });
-    meet();
-    scales_load(1);
     if (NK == 1) clear_tail(mbuf0);
+    b += gridDim.x;
+    const TileAt next = find_tile<BM, BN>(P, groups, NT, b);
+    if (next.e >= 0) look(next);
     read_scales(s0, 0);
     each<kReads>([&](auto r) { read(r, h0, mbuf0, nbuf0, 0); });
     int k = 0;
     for (; k + 4 < NK; k += 2) {  // steps k and k + 1; k + 2 and k + 3, requested here, are not the last
         multiply(First{}, Alone{}, h0, s0, h1, mbuf0, nbuf0, 0, mbuf0, nbuf0);
-        meet();
+        if (k == 0)
+            meet(Const<63>{});  // step 1 was there already: no wait for the results' stores
+        else
+            meet(All{});
         read_scales(s1, k + 1);
         multiply(Second{}, Turn{}, h1, s0, h0, mbuf1, nbuf1, k + 2, mbuf0, nbuf0);
         multiply(First{}, Alone{}, h0, s1, h1, mbuf1, nbuf1, 0, mbuf0, nbuf0);
-        meet();
+        meet(All{});
+        settle();
         read_scales(s0, k + 2);
         multiply(Second{}, Request{}, h1, s1, h0, mbuf0, nbuf0, k + 3, mbuf1, nbuf1);
     }
+    if (next.e >= 0) keep(par ^ 1);
     // The last one to four steps, k first.  What is read behind the last step is not used.
     for (;; k += 2) {
         multiply(First{}, Alone{}, h0, s0, h1, mbuf0, nbuf0, 0, mbuf0, nbuf0);
-        meet();
+        meet(All{});
         if (k + 2 == NK) clear_tail(mbuf1);
         read_scales(s1, k + 1);
         if (k + 2 < NK) {
-            scales_arrived((k >> 1) + 1);
-            each<4 * SQ>([&](auto j) { scale_store(j, (k >> 1) + 1); });
-            scales_load((k >> 1) + 2);
+            scales_arrived(sreg, (k >> 1) + 1);
+            each<4 * SQ>([&](auto j) { scale_store(j, sreg, (k >> 1) + 1); });
+            scales_load(sreg, (k >> 1) + 2);
             if (k + 3 == NK)
                 request_last(mbuf0, nbuf0);
             else
@@ -499,7 +545,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
         multiply(Second{}, Alone{}, h1, s0, h0, mbuf1, nbuf1, 0, mbuf0, nbuf0);
         if (k + 1 >= NK) break;
         multiply(First{}, Alone{}, h0, s1, h1, mbuf1, nbuf1, 0, mbuf0, nbuf0);
-        meet();
+        meet(All{});
         if (k + 3 == NK) clear_tail(mbuf0);
         read_scales(s0, k + 2);
         if (k + 4 == NK) request_last(mbuf1, nbuf1);
@@ -509,37 +555,50 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void product_tile_
     mfma_done();
 
     // No wave needs this tile's LDS any more (all passed the last meeting): the next tile's first steps.
-    const TileAt done = T;
-    b += gridDim.x;
-    T = find_tile<BM, BN>(P, groups, NT, b);
-    if (T.e >= 0) {
-        set_tile(T, par ^ 1);
+    if (next.e >= 0) {
+        set_tile(next, par ^ 1);
         request_first();
     }
+    __builtin_amdgcn_sched_barrier(0);
+    // Results: stores through a buffer that ends with the tile's last entry; columns past N are sent beyond it.
+    const int ln = fresh(), mfirst = wm + (ln & 15), nfirst = T.n0 + wn + (ln >> 4) * 8;
+    const int32_t rowOut = P.N * (OUT32 ? 4 : 2);
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<uint8_t *>(P.out) + (int64_t)T.m0 * rowOut, 0, (T.hi - T.m0) * rowOut, 0x00020000);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-        const int32_t ent = done.m0 + mrow + j * 16;
-        if (ent >= done.hi) continue;
-        const float w = factor[par][mrow + j * 16];
-        const bool none = __float_as_uint(w) == kNoRow;
+        const float w = factor[par][mfirst + j * 16];
+        const bool none = rows[par][mfirst + j * 16] < 0;
 #pragma unroll
         for (int p = 0; p < FN / 2; ++p) {
             float v[8];
+            asm volatile("" : "+a"(acc[2 * p][j]), "+a"(acc[2 * p + 1][j]));  // not copied out before they are needed
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = none ? 0.0f : acc[2 * p + (i >> 2)][j][i & 3] * w;
-            const int32_t n = done.n0 + wn + p * 32 + kb * 8;
-            const int64_t o = (int64_t)ent * P.N + n;
-            if (OUT32) {
-                float *out = static_cast<float *>(P.out) + o;
-                if (n < P.N) *reinterpret_cast<f32x4 *>(out) = f32x4{v[0], v[1], v[2], v[3]};
-                if (n + 4 < P.N) *reinterpret_cast<f32x4 *>(out + 4) = f32x4{v[4], v[5], v[6], v[7]};
-            } else if (n < P.N) {
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.out) + o) =
-                    u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+            for (int i = 0; i < 8; ++i) v[i] = acc[2 * p + (i >> 2)][j][i & 3] * w;
+            if (__any(none)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = none ? 0.0f : v[i];
             }
+            const int32_t n = nfirst + p * 32;
+            const int32_t at = (mfirst + j * 16) * rowOut + n * (OUT32 ? 4 : 2), outside = 0x7ffffff0;
+            if (OUT32) {
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                             __float_as_uint(v[3])}, out, n < P.N ? at : outside, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                                                             __float_as_uint(v[7])}, out, n + 4 < P.N ? at + 16 : outside, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])}, out,
+                    n < P.N ? at : outside, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (T.e < 0) return;
+    if (next.e < 0) return;
+    T = next;
+    begin();
+    meet(Const<kStoresLeft>{});
+    settle();
     }
 }
 
