@@ -58,71 +58,7 @@ __device__ __forceinline__ void each(F &&f) {
     }
 }
 
-// Entries of expert e, both ends inside [0, maxEntries].
-__device__ __forceinline__ void group_range(const ProductParams &P, int32_t e, int32_t &lo, int32_t &hi) {
-    lo = min(max(P.offsets[e], 0), P.maxEntries);
-    hi = min(max(P.offsets[e + 1], lo), P.maxEntries);
-}
-
-// One wave per 16 columns and 32 rows of one expert; grid (column tiles, row
-// tiles, experts).  Operands straight from memory.
-template <bool OUT32>
-__global__ __launch_bounds__(256) void product_simple_kernel(ProductParams P) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int32_t e = blockIdx.z;
-    int32_t lo, hi;
-    group_range(P, e, lo, hi);
-    const int32_t n0 = (blockIdx.x * 4 + wave) * 16;
-    if (n0 >= P.N) return;
-    const int32_t col = n0 + (lane & 15);
-    const bool colIn = col < P.N;
-    const uint8_t *b = P.weights + ((int64_t)e * P.N + (colIn ? col : 0)) * P.rowBytes;
-    const uint8_t *bs = P.weightScales + ((int64_t)e * P.N + (colIn ? col : 0)) * P.words * 4;
-    for (int32_t m0 = lo + blockIdx.y * 32; m0 < hi; m0 += gridDim.y * 32) {
-        const uint8_t *a[2], *as[2];
-        bool in[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int32_t ent = m0 + i * 16 + (lane & 15);
-            int32_t r = -1;
-            if (ent < hi) r = P.entryRow ? P.entryRow[ent] : ent;
-            in[i] = r >= 0 && r < P.numRows;
-            a[i] = P.rows + (int64_t)(in[i] ? r : 0) * P.rowBytes;
-            as[i] = P.rowScales + (int64_t)(in[i] ? r : 0) * P.words * 4;
-        }
-        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        for (int32_t k = 0; k < P.rowBytes; k += 64) {
-            const int32_t at = k + (lane >> 4) * 16;
-            const bool kin = at < P.rowBytes;
-            u32x4 bv = {0, 0, 0, 0};
-            int32_t sb = 127;
-            if (kin && colIn) bv = load16<false>(b + at), sb = bs[at >> 4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                u32x4 av = {0, 0, 0, 0};
-                int32_t sa = 127;
-                if (kin && in[i]) av = load16<false>(a[i] + at), sa = as[i][at >> 4];
-                acc[i] = mfma_fp4<0, 0>(av, bv, acc[i], sa, sb);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int32_t ent = m0 + i * 16 + (lane >> 4) * 4 + j;
-                if (ent >= hi || !colIn) continue;
-                float v = acc[i][j];
-                if (P.entryWeight) v *= P.entryWeight[ent];
-                const int64_t o = (int64_t)ent * P.N + col;
-                if (OUT32)
-                    static_cast<float *>(P.out)[o] = v;
-                else
-                    static_cast<uint16_t *>(P.out)[o] = (uint16_t)bf16_rne(v);
-            }
-    }
-}
-
-typedef uint32_t u32x4_dword __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at 4-byte alignment
+typedef uint32_t u32x2_dword __attribute__((ext_vector_type(2), aligned(4)));  // 8 bytes at 4-byte alignment
 
 // 16 bytes per lane from memory into LDS at lds + lane * 16 (lds the same in
 // all lanes), counted by vmcnt: from rs' base at voff (per lane) + soff.
@@ -146,25 +82,40 @@ struct TileAt {
 };
 
 // The groups as a wave holds them, 64 experts at a time (experts e0 + lane):
-// entries [lo, hi) and the row tiles up to and with the lane's expert.
+// entries [lo, hi) and the row tiles up to and with the lane's expert.  The
+// experts are gone through from the last to the first: a group ends at the
+// smallest offset behind its start's, so that groups never share an entry,
+// whatever the offsets are.
 struct Groups {
     int32_t lo, hi, incl;
     int64_t total;  // tiles of all experts
 };
 
+// Loads the groups of experts e0 ..; `least` is the smallest offset behind
+// them (maxEntries at first) and becomes that behind e0 - 1's start.
 template <int BM>
-__device__ __forceinline__ void load_groups(const ProductParams &P, int32_t e0, Groups &g) {
-    g.lo = g.hi = 0;
-    if (e0 + (int)(threadIdx.x & 63) < P.E) group_range(P, e0 + (threadIdx.x & 63), g.lo, g.hi);
+__device__ __forceinline__ void load_groups(const ProductParams &P, int32_t e0, int32_t &least, Groups &g) {
+    const int lane = threadIdx.x & 63, e = e0 + lane;
+    int32_t end = e < P.E ? min(max(P.offsets[e + 1], 0), P.maxEntries) : P.maxEntries;
+    g.lo = e < P.E ? min(max(P.offsets[e], 0), P.maxEntries) : P.maxEntries;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_down(end, d);
+        if (lane + d < 64) end = min(end, o);
+    }
+    end = min(end, least);
+    g.hi = e < P.E ? max(end, g.lo) : g.lo;
     g.incl = wave_incl_scan((g.hi - g.lo + BM - 1) / BM);
+    least = uniform(min(end, g.lo));  // of lane 0
 }
 
 template <int BM>
 __device__ __forceinline__ Groups count_tiles(const ProductParams &P, int32_t NT) {
     Groups g;
     int64_t total = 0;
-    for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
-        load_groups<BM>(P, e0, g);
+    int32_t least = P.maxEntries;
+    for (int32_t e0 = (P.E - 1) & ~63; e0 >= 0; e0 -= 64) {
+        load_groups<BM>(P, e0, least, g);
         total += uniform(__shfl(g.incl, 63));
     }
     g.total = total * NT;
@@ -174,7 +125,8 @@ __device__ __forceinline__ Groups count_tiles(const ProductParams &P, int32_t NT
 // Tile b among all experts' tiles (BM entries x BN columns), or e = -1 when
 // there are fewer.  Each XCD (block b % 8) takes a contiguous stretch of the
 // tiles, so the tiles that run on it together share operands in its L2;
-// within an expert, up to four row tiles go through the columns together.
+// within an expert, bands of four row tiles (up to seven where four would
+// leave a rest) go through the columns together.
 template <int BM, int BN>
 __device__ __forceinline__ TileAt find_tile(const ProductParams &P, Groups &g, int32_t NT, int32_t b) {
     const int64_t per = (g.total + 7) / 8;
@@ -182,22 +134,173 @@ __device__ __forceinline__ TileAt find_tile(const ProductParams &P, Groups &g, i
     TileAt t{-1, 0, 0, 0};
     if ((b >> 3) >= per || at >= g.total) return t;
     int64_t before = 0;
-    for (int32_t e0 = 0; e0 < P.E; e0 += 64) {
-        if (P.E > 64) load_groups<BM>(P, e0, g);
+    int32_t least = P.maxEntries;
+    for (int32_t e0 = (P.E - 1) & ~63; e0 >= 0; e0 -= 64) {
+        if (P.E > 64) load_groups<BM>(P, e0, least, g);
         const uint64_t past = __ballot((before + g.incl) * NT > at);
         if (past) {
             const int f = __builtin_ctzll(past);
             const int32_t lo = __builtin_amdgcn_readlane(g.lo, f), hi = __builtin_amdgcn_readlane(g.hi, f);
             const int32_t tiles = (hi - lo + BM - 1) / BM;
             const int32_t r0 = (int32_t)(at - (before + __builtin_amdgcn_readlane(g.incl, f) - tiles) * NT);  // inside the expert
-            const int32_t band = r0 / (4 * NT), rows = min(4, tiles - band * 4), r = r0 - band * 4 * NT;
-            const int32_t n = r / rows, m = band * 4 + r - n * rows;
+            const int32_t size = ceil_div(tiles, max(tiles >> 2, 1));  // row tiles of a band
+            const int32_t band = r0 / (size * NT), rows = min(size, tiles - band * size), r = r0 - band * size * NT;
+            const int32_t n = r / rows, m = band * size + r - n * rows;
             t = TileAt{uniform(e0 + f), uniform(lo + m * BM), uniform(min(hi, lo + m * BM + BM)), uniform(n * BN)};
             return t;
         }
         before += uniform(__shfl(g.incl, 63));
     }
     return t;
+}
+
+// Few entries per expert: the weights are streamed once, at the rate of the
+// memory.  A block takes 16 FN columns and 16 FM entries of one expert; its
+// four waves share the row's elements out among them (256-element chunks in
+// turn) and add their sums up at the end, in LDS, in wave order.  No wave needs
+// another's operands, so they go straight from memory into registers, DEPTH
+// chunks ahead, with no barrier on the way.
+//
+// A lane's scale byte is byte l / 16 of its row's word: one shift.
+template <int FM, int FN, int DEPTH, bool OUT32>
+__global__ __launch_bounds__(256) void product_stream_kernel(ProductParams P) {
+    constexpr int BM = 16 * FM, BN = 16 * FN;
+    __shared__ __attribute__((aligned(16))) float part[4][BM][BN + 4];  // + 4: rows on other banks
+    __shared__ int32_t rows[BM];
+    const int32_t NT = ceil_div(P.N, BN);
+    Groups groups = count_tiles<BM>(P, NT);
+    const TileAt T = find_tile<BM, BN>(P, groups, NT, blockIdx.x);
+    if (T.e < 0) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r16 = lane & 15, kb = lane >> 4;
+    const uint8_t *m[FM], *ms[FM];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+        const int32_t ent = min(T.m0 + f * 16 + r16, T.hi - 1);
+        const int32_t r = P.entryRow ? P.entryRow[ent] : ent;
+        const bool in = (uint32_t)r < (uint32_t)P.numRows;
+        if (wave == 0 && kb == 0) rows[f * 16 + r16] = in ? r : -1;
+        m[f] = P.rows + (int64_t)(in ? r : 0) * P.rowBytes + kb * 16;
+        ms[f] = P.rowScales + (int64_t)(in ? r : 0) * P.words * 4;
+    }
+    uint32_t n[FN], ns[FN];
+    const int64_t first = (int64_t)T.e * P.N + T.n0;
+    const __amdgpu_buffer_rsrc_t nrs = buffer_of(P.weights + first * P.rowBytes), nsrs = buffer_of(P.weightScales + first * P.words * 4);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+        const int32_t c = min(f * 16 + r16, P.N - 1 - T.n0);
+        n[f] = (uint32_t)(c * P.rowBytes + kb * 16);
+        ns[f] = (uint32_t)(c * P.words * 4);
+    }
+    struct Chunk {
+        u32x4 m[FM][2], n[FN][2];
+        u32x2 sm[FM], sn[FN];
+    };
+    auto load = [&](Chunk &c, int at) {  // chunk `at`, whole
+        const int k = uniform(at * 128), w = uniform(at * 8);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            c.n[f][0] = __builtin_amdgcn_raw_buffer_load_b128(nrs, (int)n[f], k, 0);
+            c.n[f][1] = __builtin_amdgcn_raw_buffer_load_b128(nrs, (int)n[f] + 64, k, 0);
+            c.sn[f] = __builtin_amdgcn_raw_buffer_load_b64(nsrs, (int)ns[f], w, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            c.m[f][0] = load16<false>(m[f] + k);
+            c.m[f][1] = load16<false>(m[f] + k + 64);
+            c.sm[f] = *reinterpret_cast<const u32x2_dword *>(ms[f] + w);
+        }
+    };
+    auto load_tail = [&](Chunk &c, int at) {  // the last chunk, which the rows end in: zeros behind their end
+        const int k = at * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = k + h * 64 + kb * 16 < P.rowBytes;
+            const int32_t word = min(at * 2 + h, P.words - 1) * 4;
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                c.n[f][h] = __builtin_amdgcn_raw_buffer_load_b128(nrs, in ? (int)n[f] + h * 64 + k : (int)n[f] - kb * 16, 0, 0);
+                const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(nsrs, (int)ns[f] + word, 0, 0);
+                c.sn[f][h] = in ? v : 0x7f7f7f7fu;
+            }
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                const u32x4 v = load16<false>(in ? m[f] + h * 64 + k : m[f] - kb * 16);
+                c.m[f][h] = in ? v : u32x4{0, 0, 0, 0};
+                const uint32_t s = *reinterpret_cast<const uint32_t *>(ms[f] + word);
+                c.sm[f][h] = in ? s : 0x7f7f7f7fu;
+            }
+        }
+    };
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](const Chunk &c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = mfma_fp4<0, 0>(c.n[i][h], c.m[j][h], acc[i][j], (int32_t)(c.sn[i][h] >> (8 * kb)),
+                                               (int32_t)(c.sm[j][h] >> (8 * kb)));
+    };
+    const int whole = P.rowBytes / 128;                        // whole chunks
+    const int mine = whole > wave ? (whole - wave + 3) / 4 : 0;  // chunks wave, wave + 4, ...
+    Chunk c[DEPTH];
+    if (mine > 0) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(c[d], wave + 4 * min(d, mine - 1));
+        int i = 0;
+        for (; i + 2 * DEPTH <= mine; i += DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                multiply(c[d]);
+                load(c[d], wave + 4 * (i + DEPTH + d));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (i + d < mine) {
+                multiply(c[d]);
+                if (i + DEPTH + d < mine) load(c[d], wave + 4 * (i + DEPTH + d));
+            }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (i + DEPTH + d < mine) multiply(c[d]);
+    }
+    if (P.rowBytes % 128 != 0 && (whole & 3) == wave) {
+        load_tail(c[0], whole);
+        multiply(c[0]);
+    }
+    // lane: entry r16 of fragment j, columns 4 kb .. + 3 of fragment i
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) *reinterpret_cast<f32x4 *>(&part[wave][j * 16 + r16][i * 16 + kb * 4]) = acc[i][j];
+    __syncthreads();
+    constexpr int kPer = OUT32 ? 4 : 8;  // columns per thread: 16 bytes of results
+    for (int u = threadIdx.x; u < BM * BN / kPer; u += 256) {
+        const int ent = u / (BN / kPer), col = (u - ent * (BN / kPer)) * kPer;
+        if (T.m0 + ent >= T.hi || T.n0 + col >= P.N) continue;
+        float v[kPer];
+        const bool none = rows[ent] < 0;  // a row of zeros
+        const float w = P.entryWeight ? P.entryWeight[T.m0 + ent] : 1.0f;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            v[q] = ((part[0][ent][col + q] + part[1][ent][col + q]) + part[2][ent][col + q]) + part[3][ent][col + q];
+            v[q] = none ? 0.0f : v[q] * w;
+        }
+        const int64_t o = (int64_t)(T.m0 + ent) * P.N + T.n0 + col;
+        if constexpr (OUT32)
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(P.out) + o) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(P.out) + o) =
+                u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    }
 }
 
 // A BM x BN tile by four waves, each (BM/2) x (BN/2); the weights are the
@@ -621,22 +724,31 @@ hipError_t launch_tiles(const ProductParams &P, bool out32, hipStream_t stream) 
     return hipGetLastError();
 }
 
+template <int FM, int FN, int DEPTH>
+hipError_t launch_stream(const ProductParams &P, bool out32, hipStream_t stream) {
+    const int64_t tiles = ((int64_t)P.maxEntries / (16 * FM) + (P.E < P.maxEntries ? P.E : P.maxEntries)) * ceil_div(P.N, 16 * FN);
+    const int64_t blocks = (tiles + 7) / 8 * 8;
+    if (blocks > (1 << 23)) return hipErrorInvalidConfiguration;
+    const dim3 grid((uint32_t)blocks);
+    if (out32)
+        hipLaunchKernelGGL((product_stream_kernel<FM, FN, DEPTH, true>), grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL((product_stream_kernel<FM, FN, DEPTH, false>), grid, dim3(256), 0, stream, P);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_product(const ProductParams &P, bool out32, hipStream_t stream) {
     if (P.maxEntries == 0) return hipSuccess;
     const int32_t mean = ceil_div(P.maxEntries, P.E);
     const bool wide = (int64_t)P.numRows * P.rowBytes > 0xf0000000ll;
-    if (mean > 32 && wide) return launch_tiles<128, 128, true>(P, out32, stream);
+    if (mean > 64 && wide) return launch_tiles<128, 128, true>(P, out32, stream);
     if (mean > 192) return launch_tiles<256, 256, false>(P, out32, stream);
-    if (mean > 32) return launch_tiles<128, 128, false>(P, out32, stream);
-    const int32_t per = ceil_div(P.maxEntries, 32 * P.E);
-    const dim3 grid((uint32_t)ceil_div(P.N, 64), (uint32_t)(per < 1024 ? per : 1024), (uint32_t)P.E);
-    if (out32)
-        hipLaunchKernelGGL((product_simple_kernel<true>), grid, dim3(256), 0, stream, P);
-    else
-        hipLaunchKernelGGL((product_simple_kernel<false>), grid, dim3(256), 0, stream, P);
-    return hipGetLastError();
+    if (mean > 64) return launch_tiles<128, 128, false>(P, out32, stream);
+    if (mean > 32) return launch_stream<4, 2, 2>(P, out32, stream);
+    if (mean > 16) return launch_stream<2, 2, 2>(P, out32, stream);
+    return launch_stream<1, 2, 3>(P, out32, stream);
 }
 
 }  // namespace epdc

@@ -466,14 +466,16 @@ int epdc_group_experts(const epdc_cfg *cfg, int32_t rank, const int32_t *expertI
 /*
  * out[i] = w_i * (rows[r_i] . weights[e]^T) for every entry i of every group e.
  *
- * numExperts groups of entries, offsets [numExperts+1] int32 (group e holds
- * entries [offsets[e], offsets[e+1]); values are clamped to [0, maxEntries]).
+ * numExperts groups of entries, offsets [numExperts+1] int32, ascending: group
+ * e holds entries [offsets[e], offsets[e+1]).  (Values are clamped to [0,
+ * maxEntries]; where they do not ascend, a group ends at the smallest of the
+ * offsets behind its start's, so no entry is in two groups.)
  * rows [numRows][hiddenDim/2] with rowScales [numRows][S] and weights
  * [numExperts][numCols][hiddenDim/2] with weightScales [numExperts][numCols][S]
  * are fp4x2 rows as epdc_mx_quantize makes them (S =
  * epdc_mx_scale_dim(hiddenDim)); hiddenDim counts elements, a multiple of 32.
  * entryRow [maxEntries] int32 is the row r_i of entry i (NULL: r_i = i); an
- * entry whose row is outside [0, numRows) counts as a row of zeros.
+ * entry whose row is outside [0, numRows) gives a row of +0.
  * entryWeight [maxEntries] fp32 is w_i (NULL: 1).
  * out [maxEntries][numCols] of outDtype (EPDC_BF16 or EPDC_FP32); its rows
  * must be a multiple of 16 bytes; rows from offsets[numExperts] on (and rows

@@ -174,7 +174,7 @@ def product(a, b, offsets, rows, weight, n):
     E = b.shape[0]
     for e in range(E):
         lo = min(max(int(offsets[e]), 0), n)
-        hi = min(max(int(offsets[e + 1]), lo), n)
+        hi = min(max(int(min(offsets[e + 1:])), lo), n)  # the smallest offset behind the group's start
         if lo == hi:
             continue
         r = np.arange(lo, hi) if rows is None else rows[lo:hi]
