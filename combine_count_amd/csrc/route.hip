@@ -62,13 +62,17 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
         for (int i = 0; i < NPL; ++i) {
             s[i] = !(l[i] > -kInf) ? 0.0 : l[i] == top ? 1.0 : exp((double)l[i] - (double)top);
             sum += s[i];
+            __builtin_amdgcn_sched_barrier(0);  // one exponential's registers, not all of them
         }
         sum = fmax(wave_sum(sum), 1.0);  // 1 or more unless every logit is masked
 #pragma unroll
         for (int i = 0; i < NPL; ++i) s[i] /= sum;
     } else {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = !(l[i] > -kInf) ? 0.0 : 1.0 / (1.0 + exp(-(double)l[i]));
+        for (int i = 0; i < NPL; ++i) {
+            s[i] = !(l[i] > -kInf) ? 0.0 : 1.0 / (1.0 + exp(-(double)l[i]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     const bool limited = P.keep < P.G;
 #pragma unroll
@@ -139,6 +143,260 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
         const int64_t o = (int64_t)t * P.K + lane;
         P.expertIds[o] = id;
         P.weights[o] = (float)(w * (double)P.scale);
+    }
+}
+
+// ---- the fast form ----
+//
+// LPT lanes per token (16: four tokens a wave; 64), EPL experts per lane.  The
+// rounds of the selection run on one 32-bit word per expert: the order of a
+// 32-bit choice value (sigmoid + bias, or the logit itself without a bias),
+// its lowest bits replaced by the expert's complement, so that words differ, a
+// tie goes to the lower expert, and the winner of a round names itself.
+//
+// That is exact for bf16 logits (their 16 low bits are free).  Elsewhere the
+// dropped bits and the 32-bit sigmoid can put neighbours the wrong way round;
+// so
+//   * the rounds go on past the K-th until the next value is out of its reach
+//     (nearly always one round more);
+//   * the candidates found, one per lane, are valued in 64 bits and put in order
+//     by that; the same values give the weights.
+// A token that has a candidate in every lane, or whose last group kept and
+// first group left out are closer than their scores can be off, is done again
+// by route_token in 64 bits (one in ten thousand of random logits).
+//
+// Bound by instructions, not bytes: 16 lanes per token share each wave-wide
+// maximum among four tokens.  T 65521, E 256, K 8, 8 groups, bf16: 180 us with
+// route_token for every token; see the launcher for this form's times.
+
+// A 32-bit value in the order of unsigned integers (no NaN; never 0 for a number).
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+// Lanes 1 0 3 2, 2 3 0 1, 7 .. 0 of 8 and 15 .. 0 of 16: together an exchange among 16 lanes.
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+    v = max(v, dpp<kSwap1>(v));
+    v = max(v, dpp<kSwap2>(v));
+    v = max(v, dpp<kMirror8>(v));
+    v = max(v, dpp<kMirror16>(v));
+    if (LPT == 16) return v;
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+    return max(a, b);
+}
+
+template <int LPT>
+__device__ __forceinline__ double token_sum(double v) {
+#pragma unroll
+    for (int d = LPT / 2; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+template <int EPL, bool FP32>
+__device__ __forceinline__ void load_logits(const uint8_t *p, float (&x)[EPL]) {
+    if constexpr (FP32) {
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) {
+            const u32x4 v = load16<true>(p + i * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i * 4 + j] = __uint_as_float(v[j]);
+        }
+    } else if constexpr (EPL == 4) {
+        const u32x2 v = load8<true>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL / 8; ++i) {
+            const u32x4 v = load16<true>(p + i * 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i * 8 + j] = __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
+        }
+    }
+}
+
+// VEC: E = 16 EPL and 16-byte aligned logits: a lane's experts are EPL in a
+// row (so groups are whole lanes); else experts l, l + LPT, ...
+// MODE: the scores (a compile-time choice for its registers: a softmax that is
+// not renormalised takes a sum of 64-bit exponentials over all experts).
+constexpr int kSigmoid = 0, kSoftmaxRenorm = 1, kSoftmax = 2;
+
+template <int LPT, int EPL, bool VEC, bool FP32, int MODE>
+__global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
+    extern __shared__ double route_keys[];
+    constexpr int kTokens = 64 / LPT;
+    constexpr uint32_t kIndex = LPT * EPL - 1;  // the bits that hold the expert
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (LPT - 1), row0 = lane - l;
+    const bool biased = P.bias != nullptr, limited = P.keep < P.G, sums = P.groupTop == 2;
+    const int lanesPerGroup = limited ? P.perGroup / EPL : 1;
+    const bool scored = biased || (limited && sums);  // 32-bit scores are needed
+    float bias[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) bias[i] = 0.0f;
+    if (biased) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) bias[i] = P.bias[VEC ? l * EPL + i : min(i * LPT + l, P.E - 1)];
+    }
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * kTokens; t0 < P.T; t0 += (int64_t)gridDim.x * 4 * kTokens) {
+        const bool live = t0 + lane / LPT < P.T;
+        const int64_t t = live ? t0 + lane / LPT : P.T - 1;
+        float x[EPL];
+        if constexpr (VEC) {
+            load_logits<EPL, FP32>(static_cast<const uint8_t *>(P.logits) + (t * P.E + l * EPL) * (FP32 ? 4 : 2), x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                x[i] = i * LPT + l < P.E ? load_logit<FP32>(P.logits, t * P.E + i * LPT + l) : -kInf;
+        }
+        float top = -kInf;  // the token's largest logit (softmax)
+        if constexpr (MODE != kSigmoid) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) top = fmaxf(top, x[i]);
+            const uint32_t o = token_max<LPT>(order_of(top));
+            top = value_of(o);
+        }
+        // choice values; -inf where masked (NaN compares false)
+        float c[EPL];
+        if (scored) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float v = MODE != kSigmoid ? (x[i] == top ? 1.0f : __expf(x[i] - top)) : __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+                const float u = v + bias[i];
+                c[i] = (x[i] > -kInf) & (u > -kInf) ? u : -kInf;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = x[i] > -kInf ? x[i] + 0.0f : -kInf;  // -0 as +0
+        }
+        bool close = false;  // to be done again in 64 bits
+        bool kept = true;    // the lane's group
+        if (limited) {
+            float a = -kInf, b = -kInf;  // the group's two best
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                b = __builtin_amdgcn_fmed3f(a, b, c[i]);
+                a = fmaxf(a, c[i]);
+            }
+            for (int d = 1; d < lanesPerGroup; d <<= 1) {
+                const float oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            if (sums && b > -kInf) a += b;
+            int better = 0;  // lanes of groups that go before this one
+            for (int r = lanesPerGroup; r < LPT; r += lanesPerGroup) {
+                const int from = (l + r) & (LPT - 1);
+                const float o = __shfl(a, row0 + from);
+                better += (o > a || (o == a && from < l)) ? 1 : 0;
+            }
+            kept = better < P.keep;
+            if (scored) {
+                // The last group kept and the first left out.  A score: the exponential, the sum and the reciprocal (1 ulp
+                // each, and the exponential's argument) under 2^-22 together, the bias' addition half an ulp; a group's
+                // sum of two, another half ulp.
+                const float in = value_of(~token_max<LPT>(kept ? ~order_of(a) : 0u));
+                const float out = value_of(token_max<LPT>(kept ? order_of(-kInf) : order_of(a)));
+                if (out > -kInf && !(in - out > 0x1p-21f * fmaxf(fabsf(in), fabsf(out)) + 0x1p-20f)) close = true;
+            }
+        }
+        uint32_t key[EPL], rest = kIndex - (VEC ? l * EPL : l);  // less i (times LPT): the expert's complement
+        asm volatile("" : "+v"(rest));  // not EPL registers kept from token to token
+        if (scored && !biased) {  // sums of scores for the groups, but experts go by their logits
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = c[i] > -kInf ? x[i] + 0.0f : -kInf;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            key[i] = (c[i] > -kInf) & kept ? (order_of(c[i]) & ~kIndex) | (rest - (VEC ? i : i * LPT)) : 0u;
+        // Lane k: the k-th best.  K rounds; where words are not exact, more of them until the token's next one is out of
+        // reach of its K-th: dropped bits, kIndex + 1 steps of 2^-23 each, and with a bias the scores' error as above.
+        constexpr bool kExact = !FP32;  // of a logit: 16 bits of it, at most 10 of the expert
+        const bool exact = kExact && !biased;
+        uint32_t win = 0, last = 0;
+        int rounds = 0;
+        for (int k = 0; k < LPT; ++k) {
+            uint32_t m = key[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
+            m = token_max<LPT>(m);
+            if (l == k) win = m;
+            if (k == P.K - 1) last = m;
+            rounds = k + 1;
+            if (k >= P.K) {
+                const float vi = value_of(last & ~kIndex), vo = value_of(m & ~kIndex);
+                const float off = biased ? 3.0f * (kIndex + 1) * 0x1p-23f * fmaxf(fabsf(vi), fabsf(vo)) + 0x1p-20f : 0.0f;
+                const bool open = m != 0 && !(vi - vo > off);
+                if (!__any(open)) break;
+                if (k == LPT - 1) close = close || open;
+            } else if (exact && k == P.K - 1) {
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = key[i] == m ? 0u : key[i];
+        }
+        {  // any lane's doubt is the token's
+            const uint64_t doubts = __ballot(close);
+            close = LPT == 64 ? doubts != 0 : (doubts >> row0 & 0xffff) != 0;
+        }
+        // in 64 bits: the candidates' scores, and what they are ordered by
+        const bool found = win != 0;
+        int32_t id = found ? (int32_t)(kIndex - (win & kIndex)) : -1;
+        double s = 0.0, v = -kInf64;
+        if (found) {
+            const float xe = load_logit<FP32>(P.logits, t * P.E + id);
+            if (MODE != kSigmoid)
+                s = xe == top ? 1.0 : exp((double)xe - (double)top);
+            else
+                s = 1.0 / (1.0 + exp(-(double)xe));
+            v = biased ? s + (double)P.bias[id] : (double)xe;
+        }
+        int rank = l;
+        if (!exact) {
+            rank = 0;
+            for (int k = 0; k < rounds; ++k) {
+                const double o = __shfl(v, row0 + k);
+                const int32_t oid = __shfl(id, row0 + k);
+                rank += (o > v || (o == v && oid < id)) ? 1 : 0;
+            }
+            if (!found) rank = l;
+        }
+        if (rank >= P.K) s = 0.0;  // not among the chosen
+        double w = s;
+        if (MODE == kSoftmaxRenorm || (MODE == kSigmoid && P.renorm)) {
+            const double total = token_sum<LPT>(s);
+            w = total > 0.0 ? s / total : 0.0;
+        } else if constexpr (MODE == kSoftmax) {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                sum += !(x[i] > -kInf) ? 0.0 : x[i] == top ? 1.0 : exp((double)x[i] - (double)top);
+                __builtin_amdgcn_sched_barrier(0);  // one exponential's registers, not all of them
+            }
+            w = s / fmax(token_sum<LPT>(sum), 1.0);
+        }
+        if (live && rank < P.K) {
+            const int64_t o = t * P.K + rank;
+            P.expertIds[o] = id;
+            P.weights[o] = (float)(w * (double)P.scale);
+        }
+        uint64_t again = __ballot(close && live && l == 0);
+        while (again) {  // writes the token's results over
+            const int at = __builtin_ctzll(again);
+            again &= again - 1;
+            route_token<LPT * EPL / 64, FP32>(P, (int32_t)(t0 + at / LPT), route_keys + wave * P.E);
+        }
     }
 }
 
@@ -271,6 +529,24 @@ hipError_t launch_route_n(const RouteParams &P, bool fp32, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int LPT, int EPL, bool VEC, int MODE>
+hipError_t launch_fast_mode(const RouteParams &P, bool fp32, hipStream_t stream) {
+    const dim3 grid = token_grid(ceil_div(P.T, 64 / LPT));
+    const size_t lds = P.keep < P.G ? (size_t)4 * P.E * sizeof(double) : 0;
+    if (fp32)
+        hipLaunchKernelGGL((route_fast_kernel<LPT, EPL, VEC, true, MODE>), grid, dim3(256), lds, stream, P);
+    else
+        hipLaunchKernelGGL((route_fast_kernel<LPT, EPL, VEC, false, MODE>), grid, dim3(256), lds, stream, P);
+    return hipGetLastError();
+}
+
+template <int LPT, int EPL, bool VEC>
+hipError_t launch_fast(const RouteParams &P, bool fp32, hipStream_t stream) {
+    return !P.softmax ? launch_fast_mode<LPT, EPL, VEC, kSigmoid>(P, fp32, stream)
+           : P.renorm ? launch_fast_mode<LPT, EPL, VEC, kSoftmaxRenorm>(P, fp32, stream)
+                      : launch_fast_mode<LPT, EPL, VEC, kSoftmax>(P, fp32, stream);
+}
+
 template <int NPL>
 hipError_t launch_grad_n(const RouteGradParams &P, bool fp32, hipStream_t stream) {
     const dim3 grid = token_grid(P.T);
@@ -285,6 +561,25 @@ hipError_t launch_grad_n(const RouteGradParams &P, bool fp32, hipStream_t stream
 
 hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
     if (P.T == 0) return hipSuccess;
+    const bool limited = P.keep < P.G;
+    const bool vec = (P.E == 64 || P.E == 128 || P.E == 256) && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0;
+    // The fast form needs a choice value that 32 bits give nearly (a biased
+    // softmax's hangs on a sum over all experts), a lane for one more than K, and
+    // groups that are whole lanes.
+    const bool fast = !(P.softmax && P.bias) && (!limited || (vec && 16 % P.G == 0));
+    if (fast && P.E <= 256 && P.K < 16) {
+        if (vec)
+            return P.E == 64    ? launch_fast<16, 4, true>(P, fp32, stream)
+                   : P.E == 128 ? launch_fast<16, 8, true>(P, fp32, stream)
+                                : launch_fast<16, 16, true>(P, fp32, stream);
+        return P.E <= 64    ? launch_fast<16, 4, false>(P, fp32, stream)
+               : P.E <= 128 ? launch_fast<16, 8, false>(P, fp32, stream)
+                            : launch_fast<16, 16, false>(P, fp32, stream);
+    }
+    if (fast && !limited && P.K < 64)
+        return P.E <= 256   ? launch_fast<64, 4, false>(P, fp32, stream)
+               : P.E <= 512 ? launch_fast<64, 8, false>(P, fp32, stream)
+                            : launch_fast<64, 16, false>(P, fp32, stream);
     return P.E <= 64    ? launch_route_n<1>(P, fp32, stream)
            : P.E <= 128 ? launch_route_n<2>(P, fp32, stream)
            : P.E <= 256 ? launch_route_n<4>(P, fp32, stream)
