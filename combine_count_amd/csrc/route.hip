@@ -36,6 +36,34 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
+// A 32-bit value in the order of unsigned integers (no NaN; never 0 for a number).
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+// Lanes 1 0 3 2, 2 3 0 1, 7 .. 0 of 8 and 15 .. 0 of 16: together an exchange among 16 lanes.
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+    v = max(v, dpp<kSwap1>(v));
+    v = max(v, dpp<kSwap2>(v));
+    v = max(v, dpp<kMirror8>(v));
+    v = max(v, dpp<kMirror16>(v));
+    if (LPT == 16) return v;
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+    return max(a, b);
+}
+
 // One token by one wave, any configuration: lane holds experts lane, lane +
 // 64, ...; K rounds of a wave-wide maximum over (choice value, lower index).
 // keys: [E] doubles of LDS of this wave, used where groups are limited.
@@ -81,7 +109,7 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
         double c = s[i];
         if (biased && e < P.E) c += (double)P.bias[e];
         if (!(l[i] > -kInf) || !(c > -kInf64)) c = -kInf64;
-        key[i] = c > -kInf64 && !biased ? (double)l[i] : c;
+        key[i] = (c > -kInf64 && !biased ? (double)l[i] : c) + 0.0;  // -0 as +0
         // groups go by their best keys (one value), or by sums of choice values
         if (limited && e < P.E) keys[e] = P.groupTop == 1 ? key[i] : c;
     }
@@ -117,13 +145,12 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (key[i] > best) best = key[i], at = i * 64 + lane;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            const double ob = __shfl_xor(best, d);
-            const int oa = __shfl_xor(at, d);
-            if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-        }
-        at = uniform(at);
+        // the largest (value, lower index) of the wave: its upper half, its lower half, its index
+        const uint64_t u = (uint64_t)__double_as_longlong(best);
+        const uint64_t o = u ^ (uint64_t)((int64_t)u >> 63 | (int64_t)(1ull << 63));
+        const uint32_t hi = token_max<64>((uint32_t)(o >> 32));
+        const uint32_t lo = token_max<64>((uint32_t)(o >> 32) == hi ? (uint32_t)o : 0u);
+        at = (int)~token_max<64>(o == ((uint64_t)hi << 32 | lo) ? ~(uint32_t)at : 0u);
         if (at == 0x7fffffff) break;  // nothing left to choose
         double sv = 0.0;
 #pragma unroll
@@ -168,34 +195,6 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // Bound by instructions, not bytes: 16 lanes per token share each wave-wide
 // maximum among four tokens.  T 65521, E 256, K 8, 8 groups, bf16: 180 us with
 // route_token for every token; see the launcher for this form's times.
-
-// A 32-bit value in the order of unsigned integers (no NaN; never 0 for a number).
-__device__ __forceinline__ uint32_t order_of(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
-}
-__device__ __forceinline__ float value_of(uint32_t o) {
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
-}
-// Lanes 1 0 3 2, 2 3 0 1, 7 .. 0 of 8 and 15 .. 0 of 16: together an exchange among 16 lanes.
-constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
-
-template <int LPT>
-__device__ __forceinline__ uint32_t token_max(uint32_t v) {
-    v = max(v, dpp<kSwap1>(v));
-    v = max(v, dpp<kSwap2>(v));
-    v = max(v, dpp<kMirror8>(v));
-    v = max(v, dpp<kMirror16>(v));
-    if (LPT == 16) return v;
-    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
-    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
-    return max(a, b);
-}
 
 template <int LPT>
 __device__ __forceinline__ double token_sum(double v) {
