@@ -203,6 +203,15 @@ __device__ __forceinline__ double token_sum(double v) {
     return v;
 }
 
+// Sum over a token's 16 lanes, the same in all of them.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(dpp<kSwap1>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kSwap2>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kMirror8>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kMirror16>(__float_as_uint(v)));
+    return v;
+}
+
 template <int EPL, bool FP32>
 __device__ __forceinline__ void load_logits(const uint8_t *p, float (&x)[EPL]) {
     if constexpr (FP32) {
@@ -509,6 +518,106 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradParams P) {
     }
 }
 
+// The same for E = 16 EPL experts, at most 16 slots and 16-byte aligned rows:
+// 16 lanes per token, four tokens a wave, so that a wave's instructions (what
+// bounds the form above) serve four rows.  Slot k in lane k; the token's sums
+// per expert in LDS, the slots added one after the other (a wave's LDS
+// operations stay in order, so the order of the sum is the slots'); out as
+// 16-byte pieces, one contiguous run of the row per store.
+template <int EPL, bool FP32>
+__global__ __launch_bounds__(256) void route_grad_rows_kernel(RouteGradParams P) {
+    constexpr int E = 16 * EPL;
+    constexpr int C = EPL < (FP32 ? 4 : 8) ? EPL : (FP32 ? 4 : 8);  // experts of a lane's piece
+    constexpr int N = EPL / C;                                     // pieces of a lane: experts (i * 16 + l) * C ..
+    __shared__ __attribute__((aligned(16))) float sums[16][E + 4];
+    const int lane = threadIdx.x & 63, l = lane & 15, row0 = lane - l;
+    float *row = sums[threadIdx.x >> 4];
+    const bool dense = P.softmax && !P.renorm;
+    for (int64_t t0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6) * 4; t0 < P.T; t0 += (int64_t)gridDim.x * 16) {
+        const bool live = t0 + (lane >> 4) < P.T;
+        const int64_t t = live ? t0 + (lane >> 4) : P.T - 1;
+        int32_t id = -1;
+        float g = 0.0f, sel = -kInf;
+        if (l < P.K) {
+            id = P.expertIds[t * P.K + l];
+            g = P.dWeights[t * P.K + l] * P.scale;
+        }
+        float x[EPL];
+        if (dense) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float v[C];
+                load_logits<C, FP32>(static_cast<const uint8_t *>(P.logits) + (t * E + (i * 16 + l) * C) * (FP32 ? 4 : 2), v);
+#pragma unroll
+                for (int j = 0; j < C; ++j) x[i * C + j] = v[j];
+            }
+        }
+        if ((uint32_t)id < (uint32_t)E) sel = load_logit<FP32>(P.logits, t * E + id);
+        if (!(sel > -kInf)) id = -1;
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) *reinterpret_cast<u32x4 *>(row + (i * 16 + l) * 4) = u32x4{0, 0, 0, 0};
+        float d, dot = 0.0f;
+        if (dense) {
+            float top = -kInf;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) top = fmaxf(top, x[i]);
+            top = value_of(token_max<16>(order_of(top)));
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                x[i] = !(x[i] > -kInf) ? 0.0f : x[i] == top ? 1.0f : expf(x[i] - top);
+                sum += x[i];
+            }
+            const float inv = 1.0f / fmaxf(row_sum(sum), 1.0f);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) x[i] *= inv;
+            d = id >= 0 ? g : 0.0f;
+            dot = row_sum(id < 0 ? 0.0f : g * (sel == top ? 1.0f : expf(sel - top)) * inv);
+        } else {
+            float r, q = 1.0f;
+            if (P.softmax) {
+                const float top = value_of(token_max<16>(order_of(sel)));
+                r = id < 0 ? 0.0f : sel == top ? 1.0f : expf(sel - top);
+            } else {
+                const float e = expf(-fabsf(sel)), big = 1.0f / (1.0f + e), small = e * big;
+                r = id < 0 ? 0.0f : sel >= 0.0f ? big : small;
+                q = sel >= 0.0f ? small : big;
+            }
+            float mean = 0.0f;
+            if (P.renorm) {
+                const float total = row_sum(r);
+                r = total > 0.0f ? r / total : 0.0f;
+                mean = row_sum(id >= 0 ? g * r : 0.0f);
+            }
+            d = id >= 0 ? r * q * (g - mean) : 0.0f;
+        }
+        wave_lds_order();
+        for (int k = 0; k < P.K; ++k)
+            if (l == k && id >= 0) __hip_atomic_fetch_add(row + id, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        wave_lds_order();
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                uint32_t w[C];
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    float v = row[(i * 16 + l) * C + j];
+                    if (dense) v = x[i * C + j] * (v - dot);
+                    w[j] = FP32 ? __float_as_uint(v) : bf16_rne(v);
+                }
+                uint8_t *out = static_cast<uint8_t *>(P.dLogits) + (t * E + (i * 16 + l) * C) * (FP32 ? 4 : 2);
+                if constexpr (FP32)
+                    store16<true>(out, u32x4{w[0], w[1], w[2], w[3]});
+                else if constexpr (C == 8)
+                    store16<true>(out, u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16});
+                else
+                    store8<true>(out, u32x2{w[0] | w[1] << 16, w[2] | w[3] << 16});
+            }
+        }
+        wave_lds_order();
+    }
+}
+
 // A wave per token, up to kMaxRouteBlocks blocks of four; more tokens go round.
 constexpr int kMaxRouteBlocks = 1 << 20;
 
@@ -556,6 +665,16 @@ hipError_t launch_grad_n(const RouteGradParams &P, bool fp32, hipStream_t stream
     return hipGetLastError();
 }
 
+template <int EPL>
+hipError_t launch_grad_rows(const RouteGradParams &P, bool fp32, hipStream_t stream) {
+    const dim3 grid = token_grid(ceil_div(P.T, 4));
+    if (fp32)
+        hipLaunchKernelGGL((route_grad_rows_kernel<EPL, true>), grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL((route_grad_rows_kernel<EPL, false>), grid, dim3(256), 0, stream, P);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
@@ -588,6 +707,11 @@ hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
 
 hipError_t launch_route_grad(const RouteGradParams &P, bool fp32, hipStream_t stream) {
     if (P.T == 0) return hipSuccess;
+    if ((P.E == 64 || P.E == 128 || P.E == 256) && P.K <= 16 && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0 &&
+        reinterpret_cast<uintptr_t>(P.dLogits) % 16 == 0)
+        return P.E == 64    ? launch_grad_rows<4>(P, fp32, stream)
+               : P.E == 128 ? launch_grad_rows<8>(P, fp32, stream)
+                            : launch_grad_rows<16>(P, fp32, stream);
     return P.E <= 64    ? launch_grad_n<1>(P, fp32, stream)
            : P.E <= 128 ? launch_grad_n<2>(P, fp32, stream)
            : P.E <= 256 ? launch_grad_n<4>(P, fp32, stream)
