@@ -236,6 +236,7 @@ int epdc_group_experts(const epdc_cfg *cfg, int32_t rank, const int32_t *expertI
         P.rank = rank;
         P.tileRows = epdc::group_tile_rows(P.K);
         P.tilesPerWindow = epdc::group_tiles_per_window(P.M, P.K);
+        P.windowDiv = epdc::div_magic((uint32_t)P.M * (uint32_t)P.K);
         P.expertIds = expertIds;
         P.weights = cfg->useWeights ? weights : nullptr;
         P.recvCount = recvCount;

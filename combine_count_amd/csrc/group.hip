@@ -8,9 +8,12 @@
 //   2  place_kernel: a block sums the earlier tiles' counts (its bases) and
 //      all tiles' (the groups' starts) itself, ranks its own slots in order
 //      and writes the entries.
-// Bases come from sums, not from atomics, so the order is fixed.  With more
-// than kGroupSelfWords words of counts the sums of step 2 would read too much
-// in every block: two scan launches between them turn the counts into bases.
+// Bases come from sums, not from atomics, so the order is fixed.  Up to
+// kGroupLocalSlots slots a block counts all tiles' slots itself and step 1
+// falls away; with more than kGroupSelfWords words of counts the sums of step
+// 2 would read too much in every block, and two scan launches between turn
+// the counts into bases.  Bound by latency (a launch, loads behind loads):
+// 8 windows x 128 rows x 8 slots 9.5 us, 8 x 4096 x 8 (1.6 MB) 12.2 us.
 //
 // The order of slots inside a tile: a wave takes its quarter of the tile 64
 // slots at a time; the lanes with the same expert find each other by a ballot
@@ -48,16 +51,31 @@ __device__ __forceinline__ Tile tile_of(const GroupParams &P, int32_t tile) {
     return t;
 }
 
+// The tile's slots threadIdx.x, + 256, ...: their expert in the segment, -1 for
+// none; all requested before the first is looked at.
+constexpr int kSlotsPerThread = kGroupTileSlots / (64 * kWaves);
+__device__ __forceinline__ void load_experts(const GroupParams &P, const Tile &t, int32_t (&ex)[kSlotsPerThread]) {
+#pragma unroll
+    for (int j = 0; j < kSlotsPerThread; ++j) {
+        const int32_t i = j * 256 + threadIdx.x;
+        ex[j] = i < t.live ? P.expertIds[t.slot0 + i] - t.firstExpert : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kSlotsPerThread; ++j)
+        if ((uint32_t)ex[j] >= (uint32_t)P.Epr) ex[j] = -1;
+}
+
 // Slots per expert of one tile.
 __global__ __launch_bounds__(256) void group_hist_kernel(GroupParams P) {
     extern __shared__ int32_t hist[];
     const Tile t = tile_of(P, blockIdx.x);
     for (int e = threadIdx.x; e < P.Epr; e += 256) hist[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < t.live; i += 256) {
-        const int32_t e = P.expertIds[t.slot0 + i] - t.firstExpert;
-        if ((uint32_t)e < (uint32_t)P.Epr) atomicAdd(&hist[e], 1);
-    }
+    int32_t ex[kSlotsPerThread];
+    load_experts(P, t, ex);
+#pragma unroll
+    for (int j = 0; j < kSlotsPerThread; ++j)
+        if (ex[j] >= 0) atomicAdd(&hist[ex[j]], 1);
     __syncthreads();
     int32_t *out = P.hist + (int64_t)blockIdx.x * P.Epr;
     for (int e = threadIdx.x; e < P.Epr; e += 256) out[e] = hist[e];
@@ -115,29 +133,91 @@ __global__ __launch_bounds__(256) void group_scan_groups_kernel(GroupParams P, i
     if (threadIdx.x == 0) P.offsets[groups] = carry;
 }
 
-// SELF: the block sums the tiles' counts itself; else the scan launches left
-// the bases.  LDS: cnt [kWaves][Epr], then base [Epr], then total [Epr].
-template <bool SELF>
+// Where the counts of the other tiles come from (header of this file).
+constexpr int kCountAll = 0, kSumCounts = 1, kScanned = 2;
+
+// LDS: cnt [kWaves][Epr], then base [Epr], then total [Epr].
+template <int FROM>
 __global__ __launch_bounds__(256) void group_place_kernel(GroupParams P, int32_t segTiles, int32_t bits) {
     extern __shared__ int32_t lds[];
     int32_t *cnt = lds, *base = lds + kWaves * P.Epr, *tot = base + P.Epr;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Tile t = tile_of(P, blockIdx.x);
+    // this wave's quarter of the tile's slots, 64 at a time; requested first of all
+    constexpr int kChunks = kSlotsPerThread;
+    const int32_t w0 = wave * (kChunks * 64);
+    int32_t ex[kChunks], rk[kChunks];
+    float wt[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int32_t i = w0 + c * 64 + lane;
+        ex[c] = i < t.slots ? P.expertIds[t.slot0 + i] : -1;
+        wt[c] = P.weights && i < t.slots ? P.weights[t.slot0 + i] : 0.0f;
+    }
     for (int e = threadIdx.x; e < (kWaves + 2) * P.Epr; e += 256) lds[e] = 0;
     __syncthreads();
     const int32_t groups0 = t.segment * P.Epr;
-    if (SELF) {
+    if (FROM != kScanned) {
         int32_t before = 0;  // entries of the segments in front
-        const int64_t seg0 = (int64_t)t.segTile0 * P.Epr;
-        for (int64_t i = threadIdx.x; i < seg0; i += 256) before += P.hist[i];
-        const int32_t words = segTiles * P.Epr, mine = (blockIdx.x - t.segTile0) * P.Epr;
-        for (int32_t i = threadIdx.x; i < words; i += 256) {
-            const int32_t v = P.hist[seg0 + i];
-            if (v == 0) continue;
-            const int32_t e = i % P.Epr;
-            atomicAdd(&tot[e], v);
-            if (i < mine) atomicAdd(&base[e], v);
+        const int32_t mine = (blockIdx.x - t.segTile0) * P.Epr;
+        if (FROM == kCountAll) {
+            // all slots in order, up to the segment's end
+            __shared__ int32_t live[64];  // slots of valid rows, per window
+            if ((int)threadIdx.x < P.W)
+                live[threadIdx.x] = P.K * (P.recvCount ? min(max(P.recvCount[threadIdx.x], 0), P.M) : P.M);
+            __syncthreads();
+            const int32_t slots = P.M * P.K, end = (P.rank < 0 ? t.window + 1 : P.W) * slots;
+            for (int32_t i0 = 0; i0 < end; i0 += 256 * 16) {
+                int32_t id[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int32_t i = i0 + j * 256 + threadIdx.x;
+                    id[j] = i < end ? P.expertIds[i] : -1;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int32_t i = i0 + j * 256 + threadIdx.x;
+                    const int32_t w = min((int32_t)div_by((uint32_t)i, P.windowDiv), P.W - 1);
+                    const int32_t e = id[j] - (P.rank < 0 ? w : P.rank) * P.Epr;
+                    if (i >= end || (uint32_t)e >= (uint32_t)P.Epr || i - w * slots >= live[w]) continue;
+                    if (P.rank < 0 && w < t.segment) {
+                        ++before;
+                    } else {
+                        atomicAdd(&tot[e], 1);
+                        if (i < t.slot0) atomicAdd(&base[e], 1);
+                    }
+                }
+            }
+        } else {
+            const int64_t seg0 = (int64_t)t.segTile0 * P.Epr;
+            const int32_t words = segTiles * P.Epr;
+            for (int64_t i0 = 0; i0 < seg0; i0 += 256 * 8) {
+                int32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t i = i0 + j * 256 + threadIdx.x;
+                    v[j] = i < seg0 ? P.hist[i] : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) before += v[j];
+            }
+            for (int32_t i0 = 0; i0 < words; i0 += 256 * 8) {
+                int32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int32_t i = i0 + j * 256 + threadIdx.x;
+                    v[j] = i < words ? P.hist[seg0 + i] : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (v[j] == 0) continue;
+                    const int32_t i = i0 + j * 256 + threadIdx.x, e = (int32_t)((uint32_t)i % (uint32_t)P.Epr);
+                    atomicAdd(&tot[e], v[j]);
+                    if (i < mine) atomicAdd(&base[e], v[j]);
+                }
+            }
         }
+        __syncthreads();
         int32_t carry;
         block_excl_scan(before, &carry);
         for (int32_t e0 = 0; e0 < P.Epr; e0 += 256) {
@@ -157,19 +237,11 @@ __global__ __launch_bounds__(256) void group_place_kernel(GroupParams P, int32_t
     }
     __syncthreads();
 
-    // Rank the wave's quarter of the slots, in order.
-    constexpr int kChunks = kGroupTileSlots / (64 * kWaves);  // 64-slot chunks per wave
-    const int32_t w0 = wave * (kChunks * 64);
-    int32_t ex[kChunks], rk[kChunks];
+    // Rank them, in order.
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int32_t i = w0 + c * 64 + lane;
-        int32_t e = -1;
-        if (i < t.live) {
-            e = P.expertIds[t.slot0 + i] - t.firstExpert;
-            if ((uint32_t)e >= (uint32_t)P.Epr) e = -1;
-        }
-        ex[c] = e;
+        ex[c] -= t.firstExpert;
+        if (w0 + c * 64 + lane >= t.live || (uint32_t)ex[c] >= (uint32_t)P.Epr) ex[c] = -1;
     }
     int32_t *mycnt = cnt + wave * P.Epr;
 #pragma unroll
@@ -207,7 +279,7 @@ __global__ __launch_bounds__(256) void group_place_kernel(GroupParams P, int32_t
         if (ex[c] >= 0) {
             at = mycnt[ex[c]] + rk[c];
             P.entryRow[at] = (int32_t)(slot / P.K);
-            if (P.weights) P.entryWeight[at] = P.weights[slot];
+            if (P.weights) P.entryWeight[at] = wt[c];
         }
         P.entryOf[slot] = at;
     }
@@ -230,14 +302,18 @@ hipError_t launch_group(const GroupParams &P, hipStream_t stream) {
     while ((1 << bits) < P.Epr) ++bits;
     const dim3 grid((uint32_t)tiles);
     const size_t lds = (size_t)(kWaves + 2) * P.Epr * sizeof(int32_t);
+    if ((int64_t)P.W * P.M * P.K <= kGroupLocalSlots) {
+        hipLaunchKernelGGL((group_place_kernel<kCountAll>), grid, dim3(256), lds, stream, P, segTiles, bits);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(group_hist_kernel, grid, dim3(256), P.Epr * sizeof(int32_t), stream, P);
     if (tiles * P.Epr <= kGroupSelfWords) {
-        hipLaunchKernelGGL((group_place_kernel<true>), grid, dim3(256), lds, stream, P, segTiles, bits);
+        hipLaunchKernelGGL((group_place_kernel<kSumCounts>), grid, dim3(256), lds, stream, P, segTiles, bits);
     } else {
         hipLaunchKernelGGL(group_scan_tiles_kernel, dim3((uint32_t)ceil_div(groups, 256)), dim3(256), 0, stream, P, segments,
                            segTiles);
         hipLaunchKernelGGL(group_scan_groups_kernel, dim3(1), dim3(256), 0, stream, P, (int32_t)groups);
-        hipLaunchKernelGGL((group_place_kernel<false>), grid, dim3(256), lds, stream, P, segTiles, bits);
+        hipLaunchKernelGGL((group_place_kernel<kScanned>), grid, dim3(256), lds, stream, P, segTiles, bits);
     }
     return hipGetLastError();
 }

@@ -49,6 +49,7 @@ struct GroupParams {
     int32_t rank;            // -1: window w is grouped over its own PE's experts
     int32_t tileRows;        // rows of a tile; a tile lies in one window
     int32_t tilesPerWindow;
+    DivMagic windowDiv;      // by M * K
     const int32_t *expertIds;
     const float *weights;
     const int32_t *recvCount;
@@ -62,6 +63,9 @@ struct GroupParams {
 // About 2048 slots a tile: enough rows per block to fill its waves, few
 // enough tiles that a block can sum their counts itself.
 constexpr int kGroupTileSlots = 2048;
+// Launches of up to this many slots count all of them in every block (one
+// launch; 8 windows of 64 rows x 8: 8.5 us against 9.9, of 128: 11.7 against 10.7).
+constexpr int64_t kGroupLocalSlots = 4096;
 // Launches of up to this many published words sum them in every block; more
 // go through scan launches.
 constexpr int64_t kGroupSelfWords = 32768;
