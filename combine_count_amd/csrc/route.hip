@@ -403,7 +403,10 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
         while (again) {  // writes the token's results over
             const int at = __builtin_ctzll(again);
             again &= again - 1;
-            route_token<LPT * EPL / 64, FP32>(P, (int32_t)(t0 + at / LPT), route_keys + wave * P.E);
+            // the parameters afresh, opaque: nothing of this is computed ahead for the tokens that do not need it
+            const RouteParams *Q = (const RouteParams *)__builtin_amdgcn_kernarg_segment_ptr();
+            asm volatile("" : "+s"(Q));
+            route_token<LPT * EPL / 64, FP32>(*Q, (int32_t)(t0 + at / LPT), route_keys + wave * Q->E);
         }
     }
 }
