@@ -515,6 +515,91 @@ def test_expert_product_of_large_small_and_nan_scales():
     assert np.all(np.abs(got - want)[~nan] <= ((2 * H + 4) * HALF32 * mag + H * 2.0 ** -126)[~nan])
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("experts,mean,N,H", [(65, 1, 48, 256), (130, 3, 264, 96), (200, 40, 128, 128), (300, 70, 64, 64)])
+def test_expert_product_of_many_experts(experts, mean, N, H, out):
+    """More experts than a wave holds at once, in each kernel."""
+    rng = np.random.default_rng(experts)
+    check_product(list(rng.integers(0, 2 * mean + 1, experts)), N, H, out, R=50, weighted=True, seed=experts)
+
+
+@pytest.mark.parametrize("sizes", [[1, 2], [50, 60], [700, 600]])
+def test_expert_product_without_rows_gives_zeros(sizes):
+    n, N, H = sum(sizes), 512, 256
+    bq, bs, _ = random_mx(np.random.default_rng(1), 2 * N, H)
+    o = torch.full((n, N), 77.0, device="cuda")
+    w = torch.full((n,), float("nan"), device="cuda")  # a row that is not there gives +0 whatever its weight
+    epdc.epdc_expert_product(2, N, H, n, 0, None, None, dev(sizes_to_offsets(sizes)), None, w, dev(bq), dev(bs), o, epdc.EPDC_FP32)
+    torch.cuda.synchronize()
+    assert bool((o == 0).all()) and not bool(torch.signbit(o).any())
+
+
+@pytest.mark.parametrize("sizes,N", [([3, 2, 0, 1], 512), ([100, 90, 120, 110, 95, 105, 99, 101], 4096), ([300] * 8, 4096)])
+def test_expert_product_of_rows_beyond_32_bit_offsets(sizes, N):
+    """An array of rows of 4.5 GB: the rows used lie at its start, about its 4 GB mark and at its end."""
+    H, R = 8192, 1_100_000
+    rng = np.random.default_rng(2)
+    n, E = sum(sizes), len(sizes)
+    at = np.concatenate([np.arange(20), 1_048_576 + np.arange(-10, 10), R - 1 - np.arange(20)])
+    aq, as_, a = random_mx(rng, len(at), H)
+    rows = torch.zeros(R, H // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((R, H // 128), 0x7F7F7F7F, dtype=torch.int32, device="cuda")
+    rows[dev(at)], scales[dev(at)] = dev(aq), dev(as_)
+    pick = rng.integers(0, len(at), n)
+    bq, bs, b = random_mx(rng, E * N, H)
+    o = torch.empty(n, N, device="cuda")
+    epdc.epdc_expert_product(E, N, H, n, R, rows, scales, dev(sizes_to_offsets(sizes)), dev(at[pick].astype(np.int32)), None,
+                             dev(bq), dev(bs), o, epdc.EPDC_FP32)
+    torch.cuda.synchronize()
+    some = np.unique(np.concatenate([np.arange(min(n, 4)), rng.integers(0, n, 20), [n - 1]]))
+    expert = np.searchsorted(sizes_to_offsets(sizes), some, side="right") - 1
+    b = b.reshape(E, N, H)
+    for i, e in zip(some, expert):
+        want, mag = b[e] @ a[pick[i]], np.abs(b[e]) @ np.abs(a[pick[i]])
+        assert np.all(np.abs(o[int(i)].double().cpu().numpy() - want) <= (2 * H + 4) * HALF32 * mag), i
+
+
+def test_results_and_rows_beyond_4_gb():
+    """fp32 results of 4.9 GB from 300,000 entries, and quantised rows of 4.9 GB of fp32."""
+    n, N, H = 300_000, 4096, 64
+    rng = np.random.default_rng(3)
+    aq, as_, a = random_mx(rng, 1000, H)
+    bq, bs, b = random_mx(rng, N, H)
+    o = torch.zeros(n, N, device="cuda")
+    rows = (np.arange(n) % 1000).astype(np.int32)
+    epdc.epdc_expert_product(1, N, H, n, 1000, dev(aq), dev(as_), dev(np.array([0, n], dtype=np.int32)), dev(rows), None, dev(bq),
+                             dev(bs), o, epdc.EPDC_FP32)
+    q = torch.empty(n, N // 2, dtype=torch.uint8, device="cuda")
+    s = torch.empty(n, N // 128, dtype=torch.int32, device="cuda")
+    epdc.epdc_mx_quantize(1, n, N, epdc.EPDC_FP32, o, None, q, s)
+    torch.cuda.synchronize()
+    for i in (0, 1, 255, 262_143, 262_144, 262_145, n - 257, n - 1):
+        want, mag = b @ a[i % 1000], np.abs(b) @ np.abs(a[i % 1000])
+        got = o[i].double().cpu().numpy()
+        assert np.all(np.abs(got - want) <= (2 * H + 4) * HALF32 * mag), i
+        want_q, want_s = oracle.pack(*oracle.mx_quantize(got[None]))
+        np.testing.assert_array_equal(q[i].cpu().numpy(), want_q[0])
+        np.testing.assert_array_equal(s[i].cpu().numpy(), want_s[0])
+    back = torch.zeros(n, N, device="cuda")
+    epdc.epdc_mx_dequantize(1, n, N, q, s, None, back, epdc.EPDC_FP32)
+    torch.cuda.synchronize()
+    for i in (0, 262_144, n - 1):
+        want = oracle.mx_values(*oracle.unpack(q[i:i + 1].cpu().numpy(), s[i:i + 1].cpu().numpy()))
+        np.testing.assert_array_equal(back[i].double().cpu().numpy(), want[0])
+
+
+def test_the_same_call_twice_gives_the_same_bits():
+    layer = Layer(T=100, H=512, I=256, W=4, epr=8, K=4, seed=9)
+    results = []
+    for _ in range(3):
+        layer.out.zero_()
+        layer.step()
+        torch.cuda.synchronize()
+        results.append([t.clone() for t in (layer.ids, layer.wts, layer.offsets, layer.of, layer.h1, layer.out)])
+    for r in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(results[0], r))
+
+
 # ---- streams, graphs, and all of them together --------------------------------------------------------------------
 
 
