@@ -192,9 +192,11 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // first group left out are closer than their scores can be off, is done again
 // by route_token in 64 bits (one in ten thousand of random logits).
 //
-// Bound by instructions, not bytes: 16 lanes per token share each wave-wide
-// maximum among four tokens.  T 65521, E 256, K 8, 8 groups, bf16: 180 us with
-// route_token for every token; see the launcher for this form's times.
+// Bound by instructions, not bytes (about 1300 of them per wave and token
+// group, half of those the rounds): 16 lanes per token share each wave-wide
+// maximum among four tokens.  65521 tokens, 256 experts, top-8, 8 groups, bf16
+// (38 MB): 41 us, 180 with route_token for every token; 4096 tokens fp32
+// softmax 6.4 us against 13.9.
 
 template <int LPT>
 __device__ __forceinline__ double token_sum(double v) {
@@ -235,7 +237,7 @@ __device__ __forceinline__ void load_logits(const uint8_t *p, float (&x)[EPL]) {
     }
 }
 
-// VEC: E = 16 EPL and 16-byte aligned logits: a lane's experts are EPL in a
+// VEC: E = LPT * EPL and 16-byte aligned logits: a lane's experts are EPL in a
 // row (so groups are whole lanes); else experts l, l + LPT, ...
 // MODE: the scores (a compile-time choice for its registers: a softmax that is
 // not renormalised takes a sum of 64-bit exponentials over all experts).
@@ -680,6 +682,12 @@ hipError_t launch_grad_rows(const RouteGradParams &P, bool fp32, hipStream_t str
 
 }  // namespace
 
+// Up to this many tokens a whole wave takes a token of 256 experts: fewer
+// instructions one behind the other, where there are waves for it (8 groups,
+// biased, bf16; 8 / 1024 / 2048 / 4096 tokens: 5.9 / 6.3 / 6.8 / 8.4 us against
+// 6.5 / 7.5 / 7.5 / 7.6 with four tokens a wave).
+constexpr int kWaveTokens = 2048;
+
 hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
     if (P.T == 0) return hipSuccess;
     const bool limited = P.keep < P.G;
@@ -688,6 +696,7 @@ hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
     // softmax's hangs on a sum over all experts), a lane for one more than K, and
     // groups that are whole lanes.
     const bool fast = !(P.softmax && P.bias) && (!limited || (vec && 16 % P.G == 0));
+    if (fast && vec && P.E == 256 && P.T <= kWaveTokens) return launch_fast<64, 4, true>(P, fp32, stream);
     if (fast && P.E <= 256 && P.K < 16) {
         if (vec)
             return P.E == 64    ? launch_fast<16, 4, true>(P, fp32, stream)

@@ -108,11 +108,12 @@ def test_route(cfg, values, dtype):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("E,K,G,keep,top", [(256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (96, 6, 4, 2, 2)])
-def test_route_decides_near_ties_in_64_bits(E, K, G, keep, top, score):
+@pytest.mark.parametrize("T,E,K,G,keep,top", [(200, 256, 8, 8, 4, 2), (2100, 256, 8, 8, 4, 2), (200, 256, 8, 1, 1, 1),
+                                              (2100, 256, 8, 1, 1, 1), (200, 96, 6, 4, 2, 2), (200, 128, 6, 4, 2, 2),
+                                              (200, 500, 20, 1, 1, 1)])
+def test_route_decides_near_ties_in_64_bits(T, E, K, G, keep, top, score):
     """Choice values a few 2^-26 apart: equal or reversed in 32 bits."""
     rng = np.random.default_rng(5)
-    T = 200
     base = rng.standard_normal((T, 1)) * 0.5 + 1.0
     l = (base + rng.integers(-3, 4, (T, E)) * 2.0 ** -23).astype(np.float32)
     bias = (rng.integers(-3, 4, E) * 2.0 ** -26).astype(np.float32)
@@ -122,16 +123,18 @@ def test_route_decides_near_ties_in_64_bits(E, K, G, keep, top, score):
     assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * np.abs(want))
 
 
-@pytest.mark.parametrize("T", [0, 1, 2, 3, 5, 64, 65, 1023])
+@pytest.mark.parametrize("T,values", [(0, "normal"), (1, "normal"), (2, "normal"), (3, "normal"), (5, "normal"), (64, "normal"),
+                                      (65, "normal"), (1023, "normal"), (2048, "normal"), (2049, "normal"), (2051, "masked"),
+                                      (2050, "ties"), (2055, "wide")])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_route_token_counts(T, dtype):
+def test_route_token_counts(T, values, dtype):
     rng = np.random.default_rng(T)
-    t, l = logits_of("normal", T, 256, dtype, rng)
+    t, l = logits_of(values, T, 256, dtype, rng)
     bias = (0.1 * rng.standard_normal(256)).astype(np.float32)
     ids, w = run_route(256, 8, 8, 4, 2, "sigmoid", True, 1.0, dtype, t.cuda(), dev(bias))
     want_ids, want = oracle.route(l, bias, 8, False, 8, 4, 2, True, 1.0)
     np.testing.assert_array_equal(ids, want_ids)
-    assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * want)
+    assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * want + TINY["fp32"])
 
 
 @pytest.mark.parametrize("dtype,skip", [("bf16", 1), ("bf16", 4), ("fp32", 1), ("fp32", 2)])
