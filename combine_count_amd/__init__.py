@@ -1,4 +1,6 @@
-"""MI355X-native MoE expert-parallel dispatch + combine (one GPU's share).
+"""MI355X-native MoE expert-parallel dispatch + combine (one GPU's share),
+with the operators on both sides of them: routing, fp4x2 quantisation,
+grouping by expert and the experts' product.
 
 The compute path is libepdc.so (hand-written HIP for gfx950) behind the C
 ABI in include/epdc.h; this package is its Python binding.

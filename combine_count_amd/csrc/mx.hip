@@ -10,6 +10,8 @@
 // Both are bound by memory: a thread's share is 8 elements (16 bytes of bf16,
 // 32 of fp32, 4 bytes of codes), four such units in flight; a block of 32 is
 // four lanes, so its maximum takes two exchanges inside a group of four lanes.
+// 16384 x 7168 bf16: quantise 52 us (5.7 TB/s), dequantise of the same codes
+// 43 us (6.9, part of them out of the memory-side cache); 128 rows 3.5 and 3.1.
 #include "ops_internal.h"
 
 namespace epdc {

@@ -6,6 +6,12 @@
 // holds row (or column) l % 16, elements [32 (l/16), 32 (l/16) + 32) -- one
 // block, 16 bytes -- and that block's scale byte; of the result column l % 16,
 // rows 4 (l/16) .. + 3.
+//
+// Three kernels (launch_product chooses): 256x256 and 128x128 tiles through LDS
+// where experts have many entries, bound by the matrix cores (32768 entries of
+// 32 experts, 4096 x 7168: 0.54 ms, 3.5 PFLOP/s; a loop of the instruction
+// alone reaches 6.7), and weights streamed into registers where they have few,
+// bound by the memory (64 entries: 79 us, 5.5 TB/s).
 #include "ops_internal.h"
 
 namespace epdc {
