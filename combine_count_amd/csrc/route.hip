@@ -15,6 +15,7 @@ namespace epdc {
 namespace {
 
 constexpr float kInf = __builtin_inff();
+constexpr float kLargest = 3.40282346638528859812e38f;
 constexpr double kInf64 = __builtin_inf();
 
 template <bool FP32>
@@ -195,7 +196,7 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // Bound by instructions, not bytes (about 1300 of them per wave and token
 // group, half of those the rounds): 16 lanes per token share each wave-wide
 // maximum among four tokens.  65521 tokens, 256 experts, top-8, 8 groups, bf16
-// (38 MB): 41 us, 180 with route_token for every token; 4096 tokens fp32
+// (38 MB): 39 us, 180 with route_token for every token; 4096 tokens fp32
 // softmax 6.4 us against 13.9.
 
 template <int LPT>
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
                 b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                 a = fmaxf(a, oa);
             }
-            if (sums && b > -kInf) a += b;
+            if (sums && b > -kInf) a = fmaxf(a + b, -kLargest);  // a sum past the range is no masked group (its neighbours are close)
             int better = 0;  // lanes of groups that go before this one
             for (int r = lanesPerGroup; r < LPT; r += lanesPerGroup) {
                 const int from = (l + r) & (LPT - 1);
@@ -396,13 +397,13 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
             }
             w = s / fmax(token_sum<LPT>(sum), 1.0);
         }
-        if (live && rank < P.K) {
+        if (live && !close && rank < P.K) {
             const int64_t o = t * P.K + rank;
             P.expertIds[o] = id;
             P.weights[o] = (float)(w * (double)P.scale);
         }
         uint64_t again = __ballot(close && live && l == 0);
-        while (again) {  // writes the token's results over
+        while (again) {
             const int at = __builtin_ctzll(again);
             again &= again - 1;
             // the parameters afresh, opaque: nothing of this is computed ahead for the tokens that do not need it
@@ -421,6 +422,14 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams P) {
         route_token<NPL, FP32>(P, (int32_t)t, route_keys + wave * P.E);
 }
 
+// A chosen sigmoid as a multiple of one that all of the token's chosen share,
+// exp(min(top, 0)), so that scores below the 32-bit range keep their shares of
+// the sum; 0 where the score is 0 in 64 bits too (and for a slot without an
+// expert, whose logit is -inf here).  big: 1 / (1 + exp(-|logit|)).
+__device__ __forceinline__ float share(float logit, float top, float big) {
+    return logit <= -709.78271f ? 0.0f : logit >= 0.0f ? big : expf(logit - fminf(top, 0.0f)) * big;
+}
+
 // One wave per token.  Slot k's expert, logit and gradient sit in lane k.
 // row: [NPL * 64] floats of LDS of this wave, the token's sums per expert.
 template <int NPL, bool FP32>
@@ -436,7 +445,7 @@ __device__ void grad_token(const RouteGradParams &P, int64_t t, float *row) {
             id = -1;
         else
             sel = load_logit<FP32>(P.logits, t * P.E + id);
-        if (!(sel > -kInf)) id = -1;
+        if (!(sel > -kInf)) id = -1, sel = -kInf;  // a NaN too
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) row[i * 64 + lane] = 0.0f;
@@ -472,6 +481,7 @@ __device__ void grad_token(const RouteGradParams &P, int64_t t, float *row) {
             const float x = expf(-fabsf(sel)), big = 1.0f / (1.0f + x), small = x * big;
             r = id < 0 ? 0.0f : sel >= 0.0f ? big : small;
             q = sel >= 0.0f ? small : big;
+            if (P.renorm) r = share(sel, wave_max(sel), big);
         }
         float dot = 0.0f;
         if (P.renorm) {
@@ -558,7 +568,7 @@ __global__ __launch_bounds__(256) void route_grad_rows_kernel(RouteGradParams P)
             }
         }
         if ((uint32_t)id < (uint32_t)E) sel = load_logit<FP32>(P.logits, t * E + id);
-        if (!(sel > -kInf)) id = -1;
+        if (!(sel > -kInf)) id = -1, sel = -kInf;  // a NaN too
 #pragma unroll
         for (int i = 0; i < EPL / 4; ++i) *reinterpret_cast<u32x4 *>(row + (i * 16 + l) * 4) = u32x4{0, 0, 0, 0};
         float d, dot = 0.0f;
@@ -587,6 +597,7 @@ __global__ __launch_bounds__(256) void route_grad_rows_kernel(RouteGradParams P)
                 const float e = expf(-fabsf(sel)), big = 1.0f / (1.0f + e), small = e * big;
                 r = id < 0 ? 0.0f : sel >= 0.0f ? big : small;
                 q = sel >= 0.0f ? small : big;
+                if (P.renorm) r = share(sel, value_of(token_max<16>(order_of(sel))), big);
             }
             float mean = 0.0f;
             if (P.renorm) {
@@ -696,7 +707,7 @@ hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
     // softmax's hangs on a sum over all experts), a lane for one more than K, and
     // groups that are whole lanes.
     const bool fast = !(P.softmax && P.bias) && (!limited || (vec && 16 % P.G == 0));
-    if (fast && vec && P.E == 256 && P.T <= kWaveTokens) return launch_fast<64, 4, true>(P, fp32, stream);
+    if (fast && vec && P.E == 256 && P.K < 64 && P.T <= kWaveTokens) return launch_fast<64, 4, true>(P, fp32, stream);
     if (fast && P.E <= 256 && P.K < 16) {
         if (vec)
             return P.E == 64    ? launch_fast<16, 4, true>(P, fp32, stream)

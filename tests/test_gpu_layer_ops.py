@@ -123,6 +123,36 @@ def test_route_decides_near_ties_in_64_bits(T, E, K, G, keep, top, score):
     assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * np.abs(want))
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("T,K", [(2048, 64), (300, 63), (2100, 64), (2100, 15), (2100, 16)])
+def test_route_of_as_many_experts_as_there_are_lanes(T, K, biased):
+    """The last choice and the first left out, closer than 32-bit words with the expert's number in them tell."""
+    rng = np.random.default_rng(K)
+    l = (rng.integers(-8, 8, (T, 256)) * 0.25 + rng.integers(0, 64, (T, 256)) * 2.0 ** -20).astype(np.float32)
+    bias = (0.25 * rng.integers(0, 2, 256)).astype(np.float32) if biased else None
+    ids, w = run_route(256, K, 1, 1, 1, "sigmoid", True, 1.0, "fp32", dev(l), None if bias is None else dev(bias))
+    want_ids, want = oracle.route(l, bias, K, False, 1, 1, 1, True, 1.0)
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [9, 2100])
+def test_route_groups_of_the_lowest_bias(T, dtype):
+    """Experts put out of reach by the lowest fp32 number are not masked: a group of them goes before a masked group,
+    and behind a group with one ordinary expert."""
+    rng = np.random.default_rng(T)
+    t, l = logits_of("normal", T, 256, dtype, rng)
+    bias = np.full(256, np.finfo(np.float32).min, dtype=np.float32)
+    bias[0:32] = -INF      # group 0: nothing
+    bias[40] = 0.5         # group 1: one ordinary expert
+    bias[96:128] = 0.25    # group 3: ordinary
+    bias[128] = -3e38      # group 4: a little better than 2, 5, 6 and 7
+    for keep in (3, 4, 7):
+        ids, _ = run_route(256, 12, 8, keep, 2, "sigmoid", True, 1.0, dtype, t.cuda(), dev(bias))
+        np.testing.assert_array_equal(ids, oracle.route(l, bias, 12, False, 8, keep, 2, True, 1.0)[0])
+
+
 @pytest.mark.parametrize("T,values", [(0, "normal"), (1, "normal"), (2, "normal"), (3, "normal"), (5, "normal"), (64, "normal"),
                                       (65, "normal"), (1023, "normal"), (2048, "normal"), (2049, "normal"), (2051, "masked"),
                                       (2050, "ties"), (2055, "wide")])
@@ -213,6 +243,35 @@ def test_route_grad_adds_up_the_slots_of_one_expert(score, renorm):
     dw = rng.standard_normal((T, K)).astype(np.float32)
     got = run_grad(E, K, score, renorm, 1.5, "fp32", t.cuda(), ids, dw)
     check_grad(got, l, ids, dw, score, renorm, 1.5, "fp32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 96, 128, 256])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_route_grad_of_slots_that_hold_masked_experts(score, renorm, E, dtype):
+    rng = np.random.default_rng(E)
+    T, K = 23, 5
+    t, _ = logits_of("normal", T, E, dtype, rng)
+    t[:, 3], t[:, 4] = np.nan, -INF
+    ids = rng.integers(5, E, (T, K)).astype(np.int32)
+    ids[::2, 1], ids[1::3, 2], ids[5] = 3, 4, 3
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    dw[0, 1] = np.nan  # and whatever its gradient is
+    got = run_grad(E, K, score, renorm, 1.5, dtype, t.cuda(), ids, dw)
+    check_grad(got, t.double().numpy(), ids, np.where(np.isnan(dw), 0, dw), score, renorm, 1.5, dtype)
+
+
+@pytest.mark.parametrize("E", [96, 128])
+def test_route_grad_of_scores_below_32_bits(E):
+    """Renormalised sigmoids of which no 32-bit value is left: their shares are (0 where 64 bits leave none either)."""
+    rng = np.random.default_rng(E)
+    T, K = 40, 6
+    l = (rng.standard_normal((T, E)) - 90.0 - 20.0 * np.arange(T)[:, None]).astype(np.float32)
+    ids = oracle.route(l, None, K, False)[0]
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    got = run_grad(E, K, "sigmoid", True, 1.5, "fp32", dev(l), ids, dw)
+    assert np.abs(got[:30]).max(1).min() > 1e-3 and not got[32:].any()
+    check_grad(got, l.astype(np.float64), ids, dw, "sigmoid", True, 1.5, "fp32")
 
 
 @pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
