@@ -87,6 +87,19 @@ struct ProductParams {
     void *out;
 };
 
+template <int I>
+struct Const {
+    static constexpr int value = I;
+};
+// f(Const<0>), ..., f(Const<N-1>): indices that are constants in f.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F &&f) {
+    if constexpr (I < N) {
+        f(Const<I>{});
+        each<N, I + 1>(f);
+    }
+}
+
 inline __device__ uint32_t div_by(uint32_t n, DivMagic d) {
     const uint32_t t = __umulhi(n, d.magic);
     return (t + ((n - t) >> d.sh1)) >> d.sh2;

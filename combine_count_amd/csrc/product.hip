@@ -51,19 +51,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-template <int I>
-struct Const {
-    static constexpr int value = I;
-};
-// f(Const<0>), ..., f(Const<N-1>): the instruction's byte choices are constants.
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void each(F &&f) {
-    if constexpr (I < N) {
-        f(Const<I>{});
-        each<N, I + 1>(f);
-    }
-}
-
 typedef uint32_t u32x2_dword __attribute__((ext_vector_type(2), aligned(4)));  // 8 bytes at 4-byte alignment
 
 // 16 bytes per lane from memory into LDS at lds + lane * 16 (lds the same in

@@ -199,6 +199,30 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // (38 MB): 39 us, 180 with route_token for every token; 4096 tokens fp32
 // softmax 6.4 us against 13.9.
 
+// The compare-exchanges that sort N values, N a power of two (Batcher's
+// odd-even merge: 5, 19 and 63 for 4, 8 and 16).
+template <int N>
+struct Network {
+    int n = 0, a[N * N / 2] = {}, b[N * N / 2] = {};
+    constexpr Network() {
+        for (int p = 1; p < N; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < N; j += 2 * k)
+                    for (int i = j; i < j + k && i + k < N; ++i)
+                        if (i / (2 * p) == (i + k) / (2 * p)) a[n] = i, b[n] = i + k, ++n;
+    }
+};
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+    constexpr Network<N> net;
+    each<net.n>([&](auto i) {
+        constexpr int a = net.a[decltype(i)::value], b = net.b[decltype(i)::value];
+        const uint32_t hi = max(v[a], v[b]), lo = min(v[a], v[b]);
+        v[a] = hi;
+        v[b] = lo;
+    });
+}
+
 template <int LPT>
 __device__ __forceinline__ double token_sum(double v) {
 #pragma unroll
@@ -331,31 +355,31 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             key[i] = (c[i] > -kInf) & kept ? (order_of(c[i]) & ~kIndex) | (rest - (VEC ? i : i * LPT)) : 0u;
+        sort_down(key);  // a lane's best is in front, and a round's winner moves up by one
         // Lane k: the k-th best.  K rounds; where words are not exact, more of them until the token's next one is out of
         // reach of its K-th: dropped bits, kIndex + 1 steps of 2^-23 each, and with a bias the scores' error as above.
         constexpr bool kExact = !FP32;  // of a logit: 16 bits of it, at most 10 of the expert
         const bool exact = kExact && !biased;
+        auto off_of = [](float a, float b) { return 3.0f * (kIndex + 1) * 0x1p-23f * fmaxf(fabsf(a), fabsf(b)) + 0x1p-20f; };
         uint32_t win = 0, last = 0;
         int rounds = 0;
+#pragma unroll 1
         for (int k = 0; k < LPT; ++k) {
-            uint32_t m = key[0];
-#pragma unroll
-            for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
-            m = token_max<LPT>(m);
+            const uint32_t m = token_max<LPT>(key[0]);
             if (l == k) win = m;
             if (k == P.K - 1) last = m;
             rounds = k + 1;
             if (k >= P.K) {
                 const float vi = value_of(last & ~kIndex), vo = value_of(m & ~kIndex);
-                const float off = biased ? 3.0f * (kIndex + 1) * 0x1p-23f * fmaxf(fabsf(vi), fabsf(vo)) + 0x1p-20f : 0.0f;
-                const bool open = m != 0 && !(vi - vo > off);
+                const bool open = m != 0 && !(vi - vo > (biased ? off_of(vi, vo) : 0.0f));
                 if (!__any(open)) break;
                 if (k == LPT - 1) close = close || open;
             } else if (exact && k == P.K - 1) {
                 break;
             }
+            const uint32_t won = key[0] == m ? ~0u : 0u;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) key[i] = key[i] == m ? 0u : key[i];
+            for (int i = 0; i < EPL; ++i) key[i] = ((i + 1 < EPL ? key[i + 1] : 0u) & won) | (key[i] & ~won);
         }
         {  // any lane's doubt is the token's
             const uint64_t doubts = __ballot(close);
@@ -373,8 +397,15 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
                 s = 1.0 / (1.0 + exp(-(double)xe));
             v = biased ? s + (double)P.bias[id] : (double)xe;
         }
-        int rank = l;
+        // the words' order is the values' wherever neighbours are further apart than they can be off
+        bool doubt = false;
         if (!exact) {
+            const uint32_t after = __shfl_down(win, 1, LPT);
+            const float vi = value_of(win & ~kIndex), vo = value_of(after & ~kIndex);
+            doubt = l + 1 < LPT && after != 0 && !(vi - vo > (biased ? off_of(vi, vo) : 0.0f));
+        }
+        int rank = l;
+        if (__any(doubt)) {
             rank = 0;
             for (int k = 0; k < rounds; ++k) {
                 const double o = __shfl(v, row0 + k);
