@@ -187,20 +187,22 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // so
 //   * the rounds go on past the K-th until the next value is out of its reach
 //     (nearly always one round more);
-//   * the candidates found, one per lane, are valued in 64 bits and put in order
-//     by that; the same values give the weights.
+//   * the candidates found, one per lane, are valued in 64 bits, and put in order
+//     by that where neighbours' words are too close to tell; the same values give
+//     the weights.
 // A token that has a candidate in every lane, or whose last group kept and
 // first group left out are closer than their scores can be off, is done again
 // by route_token in 64 bits (one in ten thousand of random logits).
 //
-// Bound by instructions, not bytes (about 1300 of them per wave and token
-// group, half of those the rounds): 16 lanes per token share each wave-wide
-// maximum among four tokens.  65521 tokens, 256 experts, top-8, 8 groups, bf16
-// (38 MB): 39 us, 180 with route_token for every token; 4096 tokens fp32
-// softmax 6.4 us against 13.9.
+// A lane sorts its experts' words once; a round then compares one word per lane
+// and moves the winner's list up by one.
+//
+// Bound by instructions, not bytes (1050 vector ones per wave of four tokens,
+// which keep the vector units busy three quarters of the time): 16 lanes per
+// token share each wave-wide maximum among four tokens.  65521 tokens, 256
+// experts, top-8, 8 groups, bf16 (38 MB): 39 us, 180 with route_token for every
+// token; 4096 tokens fp32 softmax 6.0 us against 13.9.
 
-// The compare-exchanges that sort N values, N a power of two (Batcher's
-// odd-even merge: 5, 19 and 63 for 4, 8 and 16).
 template <int N>
 struct Network {
     int n = 0, a[N * N / 2] = {}, b[N * N / 2] = {};
@@ -726,8 +728,8 @@ hipError_t launch_grad_rows(const RouteGradParams &P, bool fp32, hipStream_t str
 
 // Up to this many tokens a whole wave takes a token of 256 experts: fewer
 // instructions one behind the other, where there are waves for it (8 groups,
-// biased, bf16; 8 / 1024 / 2048 / 4096 tokens: 5.9 / 6.3 / 6.8 / 8.4 us against
-// 6.5 / 7.5 / 7.5 / 7.6 with four tokens a wave).
+// biased, bf16; 8 / 1024 / 2048 / 4096 tokens: 5.5 / 6.4 / 6.8 / 8.1 us against
+// 5.8 / 7.1 / 7.2 / 7.3 with four tokens a wave).
 constexpr int kWaveTokens = 2048;
 
 hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
