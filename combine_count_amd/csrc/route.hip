@@ -331,7 +331,11 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
                 b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                 a = fmaxf(a, oa);
             }
-            if (sums && b > -kInf) a = fmaxf(a + b, -kLargest);  // a sum past the range is no masked group (its neighbours are close)
+            float size = fabsf(a);  // the largest term of the group's score
+            if (sums && b > -kInf) {
+                size = fmaxf(size, fabsf(b));
+                a = fmaxf(a + b, -kLargest);  // a sum past the range is no masked group (its neighbours are close)
+            }
             int better = 0;  // lanes of groups that go before this one
             for (int r = lanesPerGroup; r < LPT; r += lanesPerGroup) {
                 const int from = (l + r) & (LPT - 1);
@@ -340,12 +344,15 @@ __global__ __launch_bounds__(256) void route_fast_kernel(RouteParams P) {
             }
             kept = better < P.keep;
             if (scored) {
-                // The last group kept and the first left out.  A score: the exponential, the sum and the reciprocal (1 ulp
-                // each, and the exponential's argument) under 2^-22 together, the bias' addition half an ulp; a group's
-                // sum of two, another half ulp.
-                const float in = value_of(~token_max<LPT>(kept ? ~order_of(a) : 0u));
-                const float out = value_of(token_max<LPT>(kept ? order_of(-kInf) : order_of(a)));
-                if (out > -kInf && !(in - out > 0x1p-21f * fmaxf(fabsf(in), fabsf(out)) + 0x1p-20f)) close = true;
+                // The last group kept and the first left out, each as far off as it can be.  A score: the exponential, the
+                // sum and the reciprocal (1 ulp each, and the exponential's argument) under 2^-22 together, the bias'
+                // addition half an ulp.  A group's score of two terms: twice that and half an ulp of the sum, which is
+                // 2^-21 + 2^-22 times the larger term at most -- of the term, not of the sum: terms of opposite sign
+                // cancel and their roundings stay.  Adding `off` rounds once more (2^-23 of the larger term).
+                const float off = 0x1.9p-22f * fminf(size, kLargest) + 0x1.1p-21f;
+                const float in = value_of(~token_max<LPT>(kept ? ~order_of(a - off) : 0u));
+                const float out = value_of(token_max<LPT>(kept ? order_of(-kInf) : order_of(a + off)));
+                if (out > -kInf && !(in > out)) close = true;
             }
         }
         uint32_t key[EPL], rest = kIndex - (VEC ? l * EPL : l);  // less i (times LPT): the expert's complement
