@@ -326,8 +326,10 @@ class PreparedCall:
 
     For launch loops that reuse the same buffers (a serving step, a
     benchmark): the device pointers and sizes are fixed at preparation, so a
-    call costs one ctypes call.  The buffers must stay alive and in place as
-    long as the prepared call is used; `keep` holds references to them."""
+    call costs one ctypes call.  The configuration is copied then: the buffers
+    were checked against it, and a later change to the caller's object must not
+    reach the call.  The buffers must stay alive and in place as long as the
+    prepared call is used; `keep` holds references to them."""
 
     def __init__(self, fn, args, keep):
         self._fn = fn
@@ -339,6 +341,10 @@ class PreparedCall:
         if rc != 0 and check:
             raise EpdcError(rc, epdc_last_error())
         return rc
+
+
+def _cfg_copy(cfg):
+    return type(cfg).from_buffer_copy(cfg)
 
 
 def _vp(a):
@@ -355,25 +361,25 @@ def prepare_dispatch(cfg: EpCfg, numTokens: int, x, expertIds, weights, scales, 
                     recvScales, recvCount, sendMap)
     bufs = (x, expertIds, weights, scales, recvX, recvTokIdx, recvExpertIds, recvWeights, recvScales, recvCount,
             sendMap, scratch)
-    args = [ctypes.byref(cfg), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
+    args = [ctypes.byref(_cfg_copy(cfg)), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
             ctypes.c_size_t(int(scratchBytes))]
-    return PreparedCall((_lib or load_library()).epdc_dispatch, args, (cfg, bufs))
+    return PreparedCall((_lib or load_library()).epdc_dispatch, args, bufs)
 
 
 def prepare_combine(cfg: EpCfg, numTokens: int, y, expertIds, weights, sendMap, out, outDtype=None) -> PreparedCall:
     _sizes_combine(cfg, numTokens, _out_dtype(cfg, outDtype), y, expertIds, weights, sendMap, out)
     bufs = (y, expertIds, weights, sendMap, out)
-    args = [ctypes.byref(cfg), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
+    args = [ctypes.byref(_cfg_copy(cfg)), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
             ctypes.c_int32(_out_dtype(cfg, outDtype))]
-    return PreparedCall((_lib or load_library()).epdc_combine, args, (cfg, bufs))
+    return PreparedCall((_lib or load_library()).epdc_combine, args, bufs)
 
 
 def prepare_combine_push(cfg: EpCfg, numTokens: int, y, recvExpertIds, recvWeights, recvCount, landing,
                          landScale) -> PreparedCall:
     _sizes_push(cfg, numTokens, y, recvExpertIds, recvWeights, recvCount, landing, landScale)
     bufs = (y, recvExpertIds, recvWeights, recvCount, landing, landScale)
-    args = [ctypes.byref(cfg), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs)]
-    return PreparedCall((_lib or load_library()).epdc_combine_push, args, (cfg, bufs))
+    args = [ctypes.byref(_cfg_copy(cfg)), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs)]
+    return PreparedCall((_lib or load_library()).epdc_combine_push, args, bufs)
 
 
 def prepare_combine_reduce(cfg: EpCfg, numTokens: int, landing, landScale, recvCount, sendMap, out,
@@ -381,6 +387,6 @@ def prepare_combine_reduce(cfg: EpCfg, numTokens: int, landing, landScale, recvC
     _sizes_combine(cfg, numTokens, _out_dtype(cfg, outDtype), landing, None, landScale, sendMap, out, landing=True)
     _need(recvCount, cfg.worldSize * 4, "recvCount")
     bufs = (landing, landScale, recvCount, sendMap, out)
-    args = [ctypes.byref(cfg), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
+    args = [ctypes.byref(_cfg_copy(cfg)), ctypes.c_int32(int(numTokens)), *(_vp(b) for b in bufs),
             ctypes.c_int32(_out_dtype(cfg, outDtype))]
-    return PreparedCall((_lib or load_library()).epdc_combine_reduce, args, (cfg, bufs))
+    return PreparedCall((_lib or load_library()).epdc_combine_reduce, args, bufs)

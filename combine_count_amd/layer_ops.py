@@ -49,21 +49,21 @@ def _i(v):
 
 def prepare_route(cfg: RouteCfg, numTokens: int, logits, bias, expertIds, weights) -> PreparedCall:
     T, E, K = max(int(numTokens), 0), cfg.numExperts, cfg.numExpertPerToken
-    args = [ctypes.byref(cfg), _i(numTokens),
+    args = [ctypes.byref(_b._cfg_copy(cfg)), _i(numTokens),
             _array(logits, T * E * _BYTES.get(cfg.dtype, 0), "logits", _FLOATS.get(cfg.dtype)),
             _array(bias, E * 4, "bias", "torch.float32"),
             _array(expertIds, T * K * 4, "expertIds", "torch.int32"),
             _array(weights, T * K * 4, "weights", "torch.float32")]
-    return _call("epdc_route", args, (cfg, logits, bias, expertIds, weights))
+    return _call("epdc_route", args, (logits, bias, expertIds, weights))
 
 
 def prepare_route_grad(cfg: RouteCfg, numTokens: int, logits, expertIds, dWeights, dLogits) -> PreparedCall:
     T, E, K = max(int(numTokens), 0), cfg.numExperts, cfg.numExpertPerToken
     row, kind = T * E * _BYTES.get(cfg.dtype, 0), _FLOATS.get(cfg.dtype)
-    args = [ctypes.byref(cfg), _i(numTokens), _array(logits, row, "logits", kind),
+    args = [ctypes.byref(_b._cfg_copy(cfg)), _i(numTokens), _array(logits, row, "logits", kind),
             _array(expertIds, T * K * 4, "expertIds", "torch.int32"),
             _array(dWeights, T * K * 4, "dWeights", "torch.float32"), _array(dLogits, row, "dLogits", kind)]
-    return _call("epdc_route_grad", args, (cfg, logits, expertIds, dWeights, dLogits))
+    return _call("epdc_route_grad", args, (logits, expertIds, dWeights, dLogits))
 
 
 def epdc_mx_scale_dim(cols: int) -> int:
@@ -108,14 +108,14 @@ def prepare_group_experts(cfg: EpCfg, rank: int, expertIds, weights, recvCount, 
     groups = (W if rank < 0 else 1) * max(cfg.numExpertPerRank, 0)
     n = W * M * K * 4
     w = n if cfg.useWeights else 0
-    args = [ctypes.byref(cfg), _i(rank), _array(expertIds, n, "expertIds", "torch.int32"),
+    args = [ctypes.byref(_b._cfg_copy(cfg)), _i(rank), _array(expertIds, n, "expertIds", "torch.int32"),
             _array(weights, w, "weights", "torch.float32"), _array(recvCount, W * 4, "recvCount", "torch.int32"),
             _array(offsets, (groups + 1) * 4, "offsets", "torch.int32"),
             _array(entryRow, n, "entryRow", "torch.int32"), _array(entryWeight, w, "entryWeight", "torch.float32"),
             _array(entryOf, n, "entryOf", "torch.int32"), _array(scratch, int(scratchBytes), "scratch"),
             ctypes.c_size_t(int(scratchBytes))]
     return _call("epdc_group_experts", args,
-                 (cfg, expertIds, weights, recvCount, offsets, entryRow, entryWeight, entryOf, scratch))
+                 (expertIds, weights, recvCount, offsets, entryRow, entryWeight, entryOf, scratch))
 
 
 def prepare_expert_product(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, rows, rowScales,
