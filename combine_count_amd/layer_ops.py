@@ -44,7 +44,10 @@ def _call(name: str, args, keep):
 
 
 def _i(v):
-    return ctypes.c_int32(int(v))
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{v} does not fit the 32 bits of the library's integer arguments")
+    return ctypes.c_int32(v)
 
 
 def prepare_route(cfg: RouteCfg, numTokens: int, logits, bias, expertIds, weights) -> PreparedCall:
@@ -67,7 +70,7 @@ def prepare_route_grad(cfg: RouteCfg, numTokens: int, logits, expertIds, dWeight
 
 
 def epdc_mx_scale_dim(cols: int) -> int:
-    return load_library().epdc_mx_scale_dim(int(cols))
+    return load_library().epdc_mx_scale_dim(min(max(int(cols), -1), 2 ** 31 - 1))
 
 
 def _mx_sizes(numWindows, rowsPerWindow, cols):
@@ -97,7 +100,7 @@ def prepare_mx_dequantize(numWindows: int, rowsPerWindow: int, cols: int, q, sca
 
 
 def epdc_group_scratch_bytes(cfg: EpCfg, rank: int) -> int:
-    return load_library().epdc_group_scratch_bytes(ctypes.byref(cfg), int(rank))
+    return load_library().epdc_group_scratch_bytes(ctypes.byref(cfg), _i(rank))
 
 
 def prepare_group_experts(cfg: EpCfg, rank: int, expertIds, weights, recvCount, offsets, entryRow, entryWeight, entryOf,
