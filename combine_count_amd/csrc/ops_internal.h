@@ -87,6 +87,37 @@ struct ProductParams {
     void *out;
 };
 
+// The product's kernels: weights streamed into registers in tiles of 16 or 64
+// entries, tiles of 128 x 128 (with 64-bit offsets of the rows: wide) or
+// 256 x 256 through LDS.
+enum ProductForm { kProductStream16, kProductStream64, kProductTiles128, kProductTiles128Wide, kProductTiles256 };
+
+// Which kernel, from the entries that can occur (the groups' sizes are known
+// on the device only).  Times in us, 4096 columns unless stated:
+//   * 256x256 tiles move the fewest operand bytes per product, and take over
+//     where the mean group fills a good part of one and there are tiles for
+//     two rounds of all CUs: h7168, 32 experts, 3000 / 4096 / 6144 / 32768
+//     entries 148 / 151 / 158 / 542 against 126 / 165 / 194 / 693 with
+//     128x128; 8 experts, 4096 entries (320 tiles) 100 against 94;
+//   * streamed weights where experts have a few entries and rows are long:
+//     h7168, 32 experts, 64 / 32 / 16 entries 79 / 54 / 27 against 91 / 71 / 33
+//     with 128x128 tiles (at h4096 48 against 43, h2048 37 against 27: the
+//     block's fixed cost);
+//   * and where 128x128 tiles would leave most CUs idle: h7168, one expert, 8 /
+//     32 / 64 entries 9 / 10 / 16 against 19; 8 experts, 8 entries 13 against 25;
+//     2 experts, 64 entries 14 (64-entry tiles; 20 with 16-entry ones) against 24;
+//     but 8 experts, 128 entries 32 against 28.
+inline ProductForm plan_product(int32_t E, int32_t N, int32_t H, int32_t maxEntries, int32_t numRows) {
+    const int32_t mean = ceil_div(maxEntries, E);
+    const int64_t groups = E < maxEntries ? E : maxEntries;
+    const int64_t tiles128 = (maxEntries / 128 + groups) * ceil_div(N, 128);
+    const int64_t tiles256 = (maxEntries / 256 + groups / 2) * ceil_div(N, 256);
+    if ((mean <= 4 && H >= 6144) || (mean <= 8 && tiles128 <= 288) || (mean <= 24 && tiles128 <= 160)) return kProductStream16;
+    if (tiles128 <= 160) return kProductStream64;
+    if ((int64_t)numRows * (H / 2) > 0xf0000000ll) return kProductTiles128Wide;
+    return mean >= 96 && tiles256 >= 512 ? kProductTiles256 : kProductTiles128;
+}
+
 template <int I>
 struct Const {
     static constexpr int value = I;

@@ -7,7 +7,7 @@
 // block, 16 bytes -- and that block's scale byte; of the result column l % 16,
 // rows 4 (l/16) .. + 3.
 //
-// Three kernels (launch_product chooses): 256x256 and 128x128 tiles through LDS
+// Three kernels (plan_product chooses): 256x256 and 128x128 tiles through LDS
 // where experts have many entries, bound by the matrix cores (32768 entries of
 // 32 experts, 4096 x 7168: 0.54 ms, 3.5 PFLOP/s; a loop of the instruction
 // alone reaches 6.7), and weights streamed into registers where they have few,
@@ -732,34 +732,16 @@ hipError_t launch_stream(const ProductParams &P, bool out32, hipStream_t stream)
 
 }  // namespace
 
-// Which kernel, from the entries that can occur (the groups' sizes are known
-// on the device only).  Times in us, 4096 columns unless stated:
-//   * 256x256 tiles move the fewest operand bytes per product, and take over
-//     where the mean group fills a good part of one and there are tiles for
-//     two rounds of all CUs: h7168, 32 experts, 3000 / 4096 / 6144 / 32768
-//     entries 148 / 151 / 158 / 542 against 126 / 165 / 194 / 693 with
-//     128x128; 8 experts, 4096 entries (320 tiles) 100 against 94;
-//   * streamed weights where experts have a few entries and rows are long:
-//     h7168, 32 experts, 64 / 32 / 16 entries 79 / 54 / 27 against 91 / 71 / 33
-//     with 128x128 tiles (at h4096 48 against 43, h2048 37 against 27: the
-//     block's fixed cost);
-//   * and where 128x128 tiles would leave most CUs idle: h7168, one expert, 8 /
-//     32 / 64 entries 9 / 10 / 16 against 19; 8 experts, 8 entries 13 against 25;
-//     2 experts, 64 entries 14 (64-entry tiles; 20 with 16-entry ones) against 24;
-//     but 8 experts, 128 entries 32 against 28.
 hipError_t launch_product(const ProductParams &P, bool out32, hipStream_t stream) {
     if (P.maxEntries == 0) return hipSuccess;
-    const int32_t mean = ceil_div(P.maxEntries, P.E);
-    const int64_t groups = P.E < P.maxEntries ? P.E : P.maxEntries;
-    const int64_t tiles128 = (P.maxEntries / 128 + groups) * ceil_div(P.N, 128);
-    const int64_t tiles256 = (P.maxEntries / 256 + groups / 2) * ceil_div(P.N, 256);
-    const bool wide = (int64_t)P.numRows * P.rowBytes > 0xf0000000ll;
-    if ((mean <= 4 && P.H >= 6144) || (mean <= 8 && tiles128 <= 288) || (mean <= 24 && tiles128 <= 160))
-        return launch_stream<1, 2, 3>(P, out32, stream);
-    if (tiles128 <= 160) return launch_stream<4, 2, 2>(P, out32, stream);
-    if (wide) return launch_tiles<128, 128, true>(P, out32, stream);
-    if (mean >= 96 && tiles256 >= 512) return launch_tiles<256, 256, false>(P, out32, stream);
-    return launch_tiles<128, 128, false>(P, out32, stream);
+    switch (plan_product(P.E, P.N, P.H, P.maxEntries, P.numRows)) {
+    case kProductStream16: return launch_stream<1, 2, 3>(P, out32, stream);
+    case kProductStream64: return launch_stream<4, 2, 2>(P, out32, stream);
+    case kProductTiles128: return launch_tiles<128, 128, false>(P, out32, stream);
+    case kProductTiles128Wide: return launch_tiles<128, 128, true>(P, out32, stream);
+    case kProductTiles256: return launch_tiles<256, 256, false>(P, out32, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace epdc
