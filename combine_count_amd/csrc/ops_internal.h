@@ -30,6 +30,37 @@ struct RouteGradParams {
     void *dLogits;
 };
 
+// The routing's kernel for a shape.
+struct RoutePlan {
+    int32_t lanes;    // of a token: 16 or 64 (the fast form; the gradient's form of four tokens a wave), 0: the general form
+    int32_t perLane;  // experts of a lane
+    bool inRow;       // a lane's experts lie in a row, one load; else lane, lane + lanes, ...
+};
+
+// Up to this many tokens a whole wave takes a token of 256 experts: fewer
+// instructions one behind the other, where there are waves for it (8 groups,
+// biased, bf16; 8 / 1024 / 2048 / 4096 tokens: 5.5 / 6.4 / 6.8 / 8.1 us against
+// 5.8 / 7.1 / 7.2 / 7.3 with four tokens a wave).
+constexpr int32_t kWaveTokens = 2048;
+
+inline RoutePlan plan_route(int32_t E, int32_t K, int32_t G, int32_t keep, int32_t T, bool softmax, bool biased, bool aligned) {
+    const bool limited = keep < G, inRow = (E == 64 || E == 128 || E == 256) && aligned;
+    // The fast form needs a choice value that 32 bits give nearly (a biased
+    // softmax's hangs on a sum over all experts), a lane for one more than K, and
+    // groups that are whole lanes.
+    const bool fast = !(softmax && biased) && (!limited || (inRow && 16 % G == 0));
+    if (fast && inRow && E == 256 && K < 64 && T <= kWaveTokens) return RoutePlan{64, 4, true};
+    if (fast && E <= 256 && K < 16) return RoutePlan{16, E <= 64 ? 4 : E <= 128 ? 8 : 16, inRow};
+    if (fast && !limited && K < 64) return RoutePlan{64, E <= 256 ? 4 : E <= 512 ? 8 : 16, false};
+    return RoutePlan{0, E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16, false};
+}
+
+// aligned: logits and dLogits at 16-byte borders.
+inline RoutePlan plan_route_grad(int32_t E, int32_t K, bool aligned) {
+    if ((E == 64 || E == 128 || E == 256) && K <= 16 && aligned) return RoutePlan{16, E / 16, true};
+    return RoutePlan{0, E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16, false};
+}
+
 // Rows of W windows of M rows; with rowCount only rows r < rowCount[w].
 struct MxParams {
     int64_t units;        // rows * cols / 8: 8 elements are one thread's share

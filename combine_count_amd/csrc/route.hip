@@ -203,6 +203,8 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 // experts, top-8, 8 groups, bf16 (38 MB): 39 us, 180 with route_token for every
 // token; 4096 tokens fp32 softmax 6.0 us against 13.9.
 
+// The compare-exchanges of the odd-even merge sort (Batcher, "Sorting networks
+// and their applications", 1968) of N values, N a power of two.
 template <int N>
 struct Network {
     int n = 0, a[N * N / 2] = {}, b[N * N / 2] = {};
@@ -733,53 +735,43 @@ hipError_t launch_grad_rows(const RouteGradParams &P, bool fp32, hipStream_t str
 
 }  // namespace
 
-// Up to this many tokens a whole wave takes a token of 256 experts: fewer
-// instructions one behind the other, where there are waves for it (8 groups,
-// biased, bf16; 8 / 1024 / 2048 / 4096 tokens: 5.5 / 6.4 / 6.8 / 8.1 us against
-// 5.8 / 7.1 / 7.2 / 7.3 with four tokens a wave).
-constexpr int kWaveTokens = 2048;
-
 hipError_t launch_route(const RouteParams &P, bool fp32, hipStream_t stream) {
     if (P.T == 0) return hipSuccess;
-    const bool limited = P.keep < P.G;
-    const bool vec = (P.E == 64 || P.E == 128 || P.E == 256) && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0;
-    // The fast form needs a choice value that 32 bits give nearly (a biased
-    // softmax's hangs on a sum over all experts), a lane for one more than K, and
-    // groups that are whole lanes.
-    const bool fast = !(P.softmax && P.bias) && (!limited || (vec && 16 % P.G == 0));
-    if (fast && vec && P.E == 256 && P.K < 64 && P.T <= kWaveTokens) return launch_fast<64, 4, true>(P, fp32, stream);
-    if (fast && P.E <= 256 && P.K < 16) {
-        if (vec)
-            return P.E == 64    ? launch_fast<16, 4, true>(P, fp32, stream)
-                   : P.E == 128 ? launch_fast<16, 8, true>(P, fp32, stream)
-                                : launch_fast<16, 16, true>(P, fp32, stream);
-        return P.E <= 64    ? launch_fast<16, 4, false>(P, fp32, stream)
-               : P.E <= 128 ? launch_fast<16, 8, false>(P, fp32, stream)
-                            : launch_fast<16, 16, false>(P, fp32, stream);
-    }
-    if (fast && !limited && P.K < 64)
-        return P.E <= 256   ? launch_fast<64, 4, false>(P, fp32, stream)
-               : P.E <= 512 ? launch_fast<64, 8, false>(P, fp32, stream)
-                            : launch_fast<64, 16, false>(P, fp32, stream);
-    return P.E <= 64    ? launch_route_n<1>(P, fp32, stream)
-           : P.E <= 128 ? launch_route_n<2>(P, fp32, stream)
-           : P.E <= 256 ? launch_route_n<4>(P, fp32, stream)
-           : P.E <= 512 ? launch_route_n<8>(P, fp32, stream)
-                        : launch_route_n<16>(P, fp32, stream);
+    const RoutePlan pl = plan_route(P.E, P.K, P.G, P.keep, P.T, P.softmax, P.bias != nullptr,
+                                    reinterpret_cast<uintptr_t>(P.logits) % 16 == 0);
+    if (pl.lanes == 16 && pl.inRow)
+        return pl.perLane == 4   ? launch_fast<16, 4, true>(P, fp32, stream)
+               : pl.perLane == 8 ? launch_fast<16, 8, true>(P, fp32, stream)
+                                 : launch_fast<16, 16, true>(P, fp32, stream);
+    if (pl.lanes == 16)
+        return pl.perLane == 4   ? launch_fast<16, 4, false>(P, fp32, stream)
+               : pl.perLane == 8 ? launch_fast<16, 8, false>(P, fp32, stream)
+                                 : launch_fast<16, 16, false>(P, fp32, stream);
+    if (pl.lanes == 64 && pl.inRow) return launch_fast<64, 4, true>(P, fp32, stream);
+    if (pl.lanes == 64)
+        return pl.perLane == 4   ? launch_fast<64, 4, false>(P, fp32, stream)
+               : pl.perLane == 8 ? launch_fast<64, 8, false>(P, fp32, stream)
+                                 : launch_fast<64, 16, false>(P, fp32, stream);
+    return pl.perLane == 1   ? launch_route_n<1>(P, fp32, stream)
+           : pl.perLane == 2 ? launch_route_n<2>(P, fp32, stream)
+           : pl.perLane == 4 ? launch_route_n<4>(P, fp32, stream)
+           : pl.perLane == 8 ? launch_route_n<8>(P, fp32, stream)
+                             : launch_route_n<16>(P, fp32, stream);
 }
 
 hipError_t launch_route_grad(const RouteGradParams &P, bool fp32, hipStream_t stream) {
     if (P.T == 0) return hipSuccess;
-    if ((P.E == 64 || P.E == 128 || P.E == 256) && P.K <= 16 && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0 &&
-        reinterpret_cast<uintptr_t>(P.dLogits) % 16 == 0)
-        return P.E == 64    ? launch_grad_rows<4>(P, fp32, stream)
-               : P.E == 128 ? launch_grad_rows<8>(P, fp32, stream)
-                            : launch_grad_rows<16>(P, fp32, stream);
-    return P.E <= 64    ? launch_grad_n<1>(P, fp32, stream)
-           : P.E <= 128 ? launch_grad_n<2>(P, fp32, stream)
-           : P.E <= 256 ? launch_grad_n<4>(P, fp32, stream)
-           : P.E <= 512 ? launch_grad_n<8>(P, fp32, stream)
-                        : launch_grad_n<16>(P, fp32, stream);
+    const RoutePlan pl = plan_route_grad(P.E, P.K, reinterpret_cast<uintptr_t>(P.logits) % 16 == 0 &&
+                                                       reinterpret_cast<uintptr_t>(P.dLogits) % 16 == 0);
+    if (pl.lanes == 16)
+        return pl.perLane == 4   ? launch_grad_rows<4>(P, fp32, stream)
+               : pl.perLane == 8 ? launch_grad_rows<8>(P, fp32, stream)
+                                 : launch_grad_rows<16>(P, fp32, stream);
+    return pl.perLane == 1   ? launch_grad_n<1>(P, fp32, stream)
+           : pl.perLane == 2 ? launch_grad_n<2>(P, fp32, stream)
+           : pl.perLane == 4 ? launch_grad_n<4>(P, fp32, stream)
+           : pl.perLane == 8 ? launch_grad_n<8>(P, fp32, stream)
+                             : launch_grad_n<16>(P, fp32, stream);
 }
 
 }  // namespace epdc

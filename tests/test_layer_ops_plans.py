@@ -73,3 +73,37 @@ def test_the_step_tests_of_small_groups_run_the_streaming_kernels(plan):
     assert {PRODUCT[v[0]] for v in plan("product", shapes).values()} == {"stream64"}
     shapes = [(8, 2048, 7168, 11, 8), (3, 8, 64, 6, 5), (40, 264, 1056, 83, 16)]  # of test_expert_product
     assert {PRODUCT[v[0]] for v in plan("product", shapes).values()} == {"stream16"}
+
+
+def test_the_gpu_tests_reach_every_routing_form(plan):
+    import test_gpu_route_forms as F
+    want = F.route_shapes()
+    assert plan("route", list(want)) == want
+    compiled = {(64, 4, 1)} | {(16, n, r) for n in (4, 8, 16) for r in (0, 1)} | {(64, n, 0) for n in (4, 8, 16)}
+    compiled |= {(0, n, 0) for n in (1, 2, 4, 8, 16)}
+    for softmax in (0, 1):  # of either score
+        assert {v for k, v in want.items() if k[5] == softmax} == compiled
+
+
+def test_gradient_forms(plan):
+    expect = {(64, 16, 1): (16, 4, 1), (128, 16, 1): (16, 8, 1), (256, 16, 1): (16, 16, 1), (64, 17, 1): (0, 1, 0),
+              (128, 17, 1): (0, 2, 0), (256, 17, 1): (0, 4, 0), (256, 8, 0): (0, 4, 0), (96, 6, 1): (0, 2, 0), (384, 8, 1): (0, 8, 0),
+              (1024, 9, 1): (0, 16, 0), (8, 2, 1): (0, 1, 0)}
+    assert plan("grad", list(expect)) == expect
+
+
+# (experts, topk, groups, kept, tokens, softmax, bias, aligned): (lanes, experts of a lane, in a row)
+ROUTE_EXPECT = {
+    (256, 8, 8, 4, 2048, 0, 1, 1): (64, 4, 1),
+    (256, 8, 8, 4, 2049, 0, 1, 1): (16, 16, 1),
+    (256, 8, 8, 4, 2049, 0, 1, 0): (0, 4, 0),  # groups of logits between 16-byte borders
+    (256, 8, 1, 1, 2049, 0, 1, 0): (16, 16, 0),
+    (256, 8, 1, 1, 4096, 1, 0, 1): (16, 16, 1),
+    (256, 8, 1, 1, 4096, 1, 1, 1): (0, 4, 0),  # a softmax with a bias
+    (160, 6, 8, 3, 4096, 1, 0, 1): (0, 4, 0),  # groups of 20
+    (160, 6, 8, 8, 4096, 1, 0, 1): (16, 16, 0),  # no limit
+}
+
+
+def test_route_forms(plan):
+    assert plan("route", list(ROUTE_EXPECT)) == ROUTE_EXPECT
