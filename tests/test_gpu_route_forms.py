@@ -1,12 +1,15 @@
-"""Routing through each compiled form, against the 64-bit implementation:
-every lane layout, kind of score and logits' type.  tests/test_layer_ops_plans.py
-checks on the host which form each shape gets."""
+"""Routing and its gradient through each compiled form, against the 64-bit
+implementation: every lane layout, kind of score and logits' type, the rounds
+that blocks go when there are more tokens than one grid covers, the largest K
+of the gradient's form of four tokens a wave, slots that share an expert.
+tests/test_layer_ops_plans.py checks on the host which form each shape gets."""
 import numpy as np
 import pytest
 import torch
 
+import combine_count_amd as epdc
 import layer_oracle as oracle
-from test_gpu_layer_ops import HALF32, KIND, TINY, dev, logits_of, run_route
+from test_gpu_layer_ops import HALF32, KIND, TINY, check_grad, dev, logits_of, run_grad, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +80,101 @@ def test_every_form(cfg, score, renorm, dtype):
     np.testing.assert_array_equal(ids, want_ids)
     # computed in 64 bits and rounded once: half a step, and what 64 bits are off themselves
     assert np.all(np.abs(w - want) <= HALF32 * (1 + 2.0 ** -20) * np.abs(want) + TINY["fp32"])
+
+
+GRID = 1 << 20  # the most blocks of a launch; a block takes 4 tokens, or 16 where a wave takes four
+
+# (tokens of a block, experts, topk, groups, kept, groupTop, score, bias)
+ROUNDS = [(16, 8, 2, 1, 1, 1, "sigmoid", True), (16, 64, 6, 8, 4, 2, "sigmoid", True), (4, 16, 16, 1, 1, 1, "softmax", False),
+          (4, 8, 2, 4, 2, 2, "softmax", True)]
+
+
+def round_shapes():
+    form = {16: 16, 4: 64}
+    return {(E, K, G, keep, per * GRID + 777, int(score == "softmax"), int(biased), 1):
+            0 if score == "softmax" and biased else form[per] for per, E, K, G, keep, _, score, biased in ROUNDS}
+
+
+def some_tokens(first, T, rng):
+    """Of the first round's start and end, and of the second round."""
+    return np.unique(np.concatenate([np.arange(8), first - 1 - np.arange(8), first + np.arange(T - first),
+                                     rng.integers(0, first, 30)]))
+
+
+@pytest.mark.parametrize("per,E,K,G,keep,top,score,biased", ROUNDS)
+def test_more_tokens_than_one_grid(per, E, K, G, keep, top, score, biased):
+    first = per * GRID
+    T = first + 777
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E)
+    l = torch.randint(-24, 24, (T, E), device="cuda", generator=g, dtype=torch.int16).to(torch.bfloat16) / 8  # with ties
+    bias = 0.1 * torch.randn(E, device="cuda", generator=g) if biased else None
+    cfg = epdc.RouteCfg(E, K, epdc.EPDC_BF16, epdc.EPDC_SOFTMAX if score == "softmax" else epdc.EPDC_SIGMOID, G, keep, top, 1, 1.0)
+    ids = torch.full((T + 1, K), -77, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, K), -7.0, device="cuda")
+    epdc.epdc_route(cfg, T, l, bias, ids, w)
+    part_ids, part_w = torch.empty_like(ids[:T]), torch.empty_like(w[:T])
+    for t0 in range(0, T, first // 2):  # in calls of one round each
+        n = min(first // 2, T - t0)
+        epdc.epdc_route(cfg, n, l[t0:t0 + n], bias, part_ids[t0:t0 + n], part_w[t0:t0 + n])
+    torch.cuda.synchronize()
+    assert bool((ids[T] == -77).all()) and bool((w[T] == -7.0).all())
+    assert torch.equal(ids[:T], part_ids) and torch.equal(w[:T], part_w)
+    at = some_tokens(first, T, np.random.default_rng(E))
+    x = l[dev(at)].double().cpu().numpy()
+    want_ids, want = oracle.route(x, None if bias is None else bias.cpu().numpy(), K, score == "softmax", G, keep, top, True, 1.0)
+    np.testing.assert_array_equal(ids[dev(at)].cpu().numpy(), want_ids)
+    assert np.all(np.abs(w[dev(at)].double().cpu().numpy() - want) <= HALF32 * (1 + 2.0 ** -20) * want)
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("per,E,K", [(4, 8, 2), (16, 64, 6)])
+def test_more_tokens_than_one_grid_in_the_gradient(per, E, K, score, renorm):
+    first = per * GRID
+    T = first + 777
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E)
+    l = torch.randint(-24, 24, (T, E), device="cuda", generator=g, dtype=torch.int16).to(torch.bfloat16) / 8
+    ids = torch.randint(-1, E, (T, K), device="cuda", generator=g, dtype=torch.int32)
+    dw = torch.randn(T, K, device="cuda", generator=g)
+    cfg = epdc.RouteCfg(E, K, epdc.EPDC_BF16, epdc.EPDC_SOFTMAX if score == "softmax" else epdc.EPDC_SIGMOID, 1, 1, 1, int(renorm), 1.0)
+    d = torch.full((T + 1, E), 9.0, dtype=torch.bfloat16, device="cuda")
+    epdc.epdc_route_grad(cfg, T, l, ids, dw, d)
+    part = torch.empty_like(d[:T])
+    for t0 in range(0, T, first // 2):
+        n = min(first // 2, T - t0)
+        epdc.epdc_route_grad(cfg, n, l[t0:t0 + n], ids[t0:t0 + n], dw[t0:t0 + n], part[t0:t0 + n])
+    torch.cuda.synchronize()
+    assert bool((d[T] == 9.0).all())
+    assert torch.equal(d[:T], part)
+    at = dev(some_tokens(first, T, np.random.default_rng(E)))
+    check_grad(d[at].double().cpu().numpy(), l[at].double().cpu().numpy(), ids[at].cpu().numpy(), dw[at].cpu().numpy(), score, renorm,
+               1.0, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 128, 256])
+@pytest.mark.parametrize("K", [15, 16, 17])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_gradient_around_sixteen_slots(score, renorm, K, E, dtype):
+    """Up to 16 slots: four tokens a wave, a slot in each of a token's lanes; from 17 a token a wave."""
+    rng = np.random.default_rng(E + K)
+    t, l = logits_of("normal", 45, E, dtype, rng)
+    ids = oracle.route(l, None, K, score == "softmax")[0]
+    ids[rng.random(ids.shape) < 0.1] = -1
+    dw = rng.standard_normal((45, K)).astype(np.float32)
+    check_grad(run_grad(E, K, score, renorm, 2.5, dtype, t.cuda(), ids, dw), l, ids, dw, score, renorm, 2.5, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 96, 128, 256])
+@pytest.mark.parametrize("K", [6, 16])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_gradient_of_slots_that_share_an_expert(score, renorm, K, E, dtype):
+    rng = np.random.default_rng(E + K)
+    T = 37
+    t, l = logits_of("normal", T, E, dtype, rng)
+    ids = rng.integers(E - 4, E, (T, K)).astype(np.int32)
+    ids[0], ids[1, 1:] = E - 1, -1  # all slots one expert; one slot alone
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    check_grad(run_grad(E, K, score, renorm, 1.5, dtype, t.cuda(), ids, dw), l, ids, dw, score, renorm, 1.5, dtype)

@@ -83,6 +83,8 @@ def test_the_gpu_tests_reach_every_routing_form(plan):
     compiled |= {(0, n, 0) for n in (1, 2, 4, 8, 16)}
     for softmax in (0, 1):  # of either score
         assert {v for k, v in want.items() if k[5] == softmax} == compiled
+    rounds = F.round_shapes()
+    assert {k: v[0] for k, v in plan("route", list(rounds)).items()} == rounds
 
 
 def test_gradient_forms(plan):
