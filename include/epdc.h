@@ -372,6 +372,14 @@ int epdc_route(const epdc_route_cfg *cfg, int32_t numTokens, const void *logits,
  *   sigmoid, renormalize    c r_i (1 - s_i) (g_i - sum_j g_j r_j)
  * summed over i's slots, and 0 (but for softmax without renormalize) where i
  * has none.  Computed in fp32 and rounded once (nearest, ties to even).
+ * With renormalize the shares r_k are taken among the token's slots alone: for
+ * softmax r_k = exp(l_k) / (sum of exp(l_j) over the slots), which is the
+ * weight / c of epdc_route unless the chosen s all vanish in 64 bits, where
+ * epdc_route gives weights of 0: an expert that is not in the token's slots
+ * (its bias masks it, its group was not kept, its slot was dropped) has a
+ * logit of +inf, or one 745 or more above all of theirs.  The gradient of such
+ * a token is that of the shares all the same; it does not read the logits of
+ * other experts.  To have none, give its slots id -1 or dWeights 0.
  */
 int epdc_route_grad(const epdc_route_cfg *cfg, int32_t numTokens, const void *logits,
                     const int32_t *expertIds, const float *dWeights, void *dLogits, void *stream);

@@ -178,3 +178,27 @@ def test_gradient_of_slots_that_share_an_expert(score, renorm, K, E, dtype):
     ids[0], ids[1, 1:] = E - 1, -1  # all slots one expert; one slot alone
     dw = rng.standard_normal((T, K)).astype(np.float32)
     check_grad(run_grad(E, K, score, renorm, 1.5, dtype, t.cuda(), ids, dw), l, ids, dw, score, renorm, 1.5, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [96, 128])
+@pytest.mark.parametrize("above", [float("inf"), 900.0])
+def test_softmax_shares_of_scores_that_vanish(above, E, dtype):
+    """An expert that its bias masks has a logit so far above all others that the chosen scores vanish in 64 bits: the
+    weights are 0, the gradient is that of the shares among the slots (include/epdc.h)."""
+    rng = np.random.default_rng(E)
+    T, K, scale = 21, 5, 2.0
+    l = rng.standard_normal((T, E))
+    l[:, 7] = above
+    t = torch.from_numpy(l).to(KIND[dtype][1])
+    l = t.double().numpy()
+    bias = np.zeros(E, dtype=np.float32)
+    bias[7] = -np.inf
+    bias[10:20] = 0.5
+    ids, w = run_route(E, K, 1, 1, 1, "softmax", True, scale, dtype, t.cuda(), dev(bias))
+    assert not w.any() and (ids == np.arange(10, 10 + K)).all()  # choice values all 0.5: the lowest of them
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    check_grad(run_grad(E, K, "softmax", True, scale, dtype, t.cuda(), ids, dw), l, ids, dw, "softmax", True, scale, dtype)
+    # no slot, no gradient; nor without a gradient of the weights
+    assert not run_grad(E, K, "softmax", True, scale, dtype, t.cuda(), np.full_like(ids, -1), dw).any()
+    assert not run_grad(E, K, "softmax", True, scale, dtype, t.cuda(), ids, np.zeros_like(dw)).any()
