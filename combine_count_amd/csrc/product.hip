@@ -9,9 +9,9 @@
 //
 // Three kernels (plan_product chooses): 256x256 and 128x128 tiles through LDS
 // where experts have many entries, bound by the matrix cores (32768 entries of
-// 32 experts, 4096 x 7168: 0.54 ms, 3.5 PFLOP/s; a loop of the instruction
+// 32 experts, 4096 x 7168: 0.55 ms, 3.5 PFLOP/s; a loop of the instruction
 // alone reaches 6.7), and weights streamed into registers where they have few,
-// bound by the memory (64 entries: 79 us, 5.5 TB/s).
+// bound by the memory (64 entries: 83 us, 5.2 TB/s).
 #include "ops_internal.h"
 
 namespace epdc {

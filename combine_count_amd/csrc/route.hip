@@ -192,7 +192,10 @@ __device__ void route_token(const RouteParams &P, int32_t t, double *keys) {
 //     the weights.
 // A token that has a candidate in every lane, or whose last group kept and
 // first group left out are closer than their scores can be off, is done again
-// by route_token in 64 bits (one in ten thousand of random logits).
+// by route_token in 64 bits: one in some ten thousand of random logits, but
+// every token of equal logits, or of one expert far above all others with
+// groups by their two best, then at 163 and 227 us for 65521 tokens against 31
+// and 39.
 //
 // A lane sorts its experts' words once; a round then compares one word per lane
 // and moves the winner's list up by one.

@@ -45,6 +45,8 @@
  *   - Index layout: T = numTokens, K = numExpertPerToken, W = worldSize,
  *     M = maxTokPerRank, H = hiddenDim, Epr = numExpertPerRank, E = W*Epr.
  *     All arrays are dense row-major with exactly these extents.
+ *   - An array that a call writes overlaps none that it reads, and no other
+ *     that it writes.
  */
 #ifndef EPDC_H
 #define EPDC_H
@@ -474,7 +476,7 @@ int epdc_group_experts(const epdc_cfg *cfg, int32_t rank, const int32_t *expertI
 /*
  * out[i] = w_i * (rows[r_i] . weights[e]^T) for every entry i of every group e.
  *
- * numExperts groups of entries, offsets [numExperts+1] int32, ascending: group
+ * numExperts (1..65535) groups of entries, offsets [numExperts+1] int32, ascending: group
  * e holds entries [offsets[e], offsets[e+1]).  (Values are clamped to [0,
  * maxEntries]; where they do not ascend, a group ends at the smallest of the
  * offsets behind its start's, so no entry is in two groups.)
@@ -485,15 +487,17 @@ int epdc_group_experts(const epdc_cfg *cfg, int32_t rank, const int32_t *expertI
  * entryRow [maxEntries] int32 is the row r_i of entry i (NULL: r_i = i); an
  * entry whose row is outside [0, numRows) gives a row of +0.
  * entryWeight [maxEntries] fp32 is w_i (NULL: 1).
- * out [maxEntries][numCols] of outDtype (EPDC_BF16 or EPDC_FP32); its rows
- * must be a multiple of 16 bytes; rows from offsets[numExperts] on (and rows
+ * out [maxEntries][numCols] of outDtype (EPDC_BF16 or EPDC_FP32), numCols up
+ * to 2^20; its rows must be a multiple of 16 bytes; rows from offsets[numExperts] on (and rows
  * before offsets[0]) are left untouched.
  * Products and sums are fp32 (their order is fixed for given sizes: results
  * are the same from run to run); w_i is applied to the sum, then the result is
  * rounded (nearest, ties to even).  rows, weights and out must be 16-byte
  * aligned, the other arrays 4-byte.
- * maxEntries also chooses the kernel: pass the number of entries that can
- * occur, not a far larger capacity, for the best speed.
+ * maxEntries also chooses the kernel (the groups' sizes are known on the device
+ * only): pass the number of entries that can occur, not a far larger capacity,
+ * for the best speed -- 64 entries of 32 experts, 7168 -> 4096, take half as
+ * long again where maxEntries says 8192.
  */
 int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
                         int32_t numRows, const void *rows, const void *rowScales, const int32_t *offsets,
