@@ -259,7 +259,7 @@ def _calls(st):
         return [epdc.prepare_expert_gate(1, c["cols"], n, dtype, st["h"], st["offsets"], st["w"], st["out"], out)]
     E, N, H, R = c["experts"], c["cols"], c["hidden"], c["rows"]
     if op == "product":
-        return [epdc.prepare_expert_product_bf16(E, N, H, n, R, st["x"], st["offsets"], st["entry_row"], st["w"], st["b"],
+        return [epdc.prepare_expert_linear(E, N, H, n, R, st["x"], st["offsets"], st["entry_row"], st["w"], st["b"],
                                                  st["out"], out)]
     if op == "rows_grad":
         return [epdc.prepare_expert_rows_grad(E, N, H, n, R, st["x"], st["offsets"], st["entry_row"], st["w"], st["b"],
@@ -268,10 +268,10 @@ def _calls(st):
         return [epdc.prepare_expert_weights_grad(E, N, H, n, n, st["dout"], None, R, st["x"], st["entry_row"], st["offsets"],
                                                  st["base"], st["out"], out)]
     if c["gated"]:
-        first = epdc.prepare_expert_gate_int8(E, H, n, kind[c["dtype"]], st["x"], st["offsets"], None, st["q"], st["qs"])
+        first = epdc.prepare_expert_gate_int(E, H, n, kind[c["dtype"]], st["x"], st["offsets"], None, st["q"], st["qs"])
     else:
-        first = epdc.prepare_int8_quantize(1, R, H, kind[c["dtype"]], st["x"], None, st["q"], st["qs"])
-    return [first, epdc.prepare_expert_product_int8(E, N, H, n, R, st["q"], st["qs"], st["offsets"], st["entry_row"], st["w"],
+        first = epdc.prepare_int_quantize(1, R, H, kind[c["dtype"]], st["x"], None, st["q"], st["qs"])
+    return [first, epdc.prepare_expert_linear_int(E, N, H, n, R, st["q"], st["qs"], st["offsets"], st["entry_row"], st["w"],
                                                     st["b"], st["bs"], st["out"], out)]
 
 
