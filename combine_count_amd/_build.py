@@ -13,8 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libepdc.so")
-SOURCES = ["epdc_api.cpp", "epdc_api_ops.cpp", "dispatch.hip", "combine.hip", "combine_push.hip", "route.hip", "mx.hip",
-           "group.hip", "product.hip"]
+SOURCES = ["epdc_api.cpp", "epdc_api_ops.cpp", "epdc_api_experts.cpp", "dispatch.hip", "combine.hip", "combine_push.hip",
+           "route.hip", "mx.hip", "group.hip", "product.hip", "product_dense.hip", "gate.hip", "int8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [

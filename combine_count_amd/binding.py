@@ -28,7 +28,9 @@ ERRORS = {
 EXPORTS = ("epdc_dispatch_scratch_bytes", "epdc_dispatch", "epdc_dispatch_noalloc", "epdc_combine",
            "epdc_landing_rows", "epdc_combine_push", "epdc_combine_reduce", "epdc_last_error",
            "epdc_route", "epdc_route_grad", "epdc_mx_scale_dim", "epdc_mx_quantize", "epdc_mx_dequantize",
-           "epdc_group_scratch_bytes", "epdc_group_experts", "epdc_expert_product")
+           "epdc_group_scratch_bytes", "epdc_group_experts", "epdc_expert_product", "epdc_expert_linear",
+           "epdc_expert_rows_grad", "epdc_expert_weights_grad", "epdc_expert_gate", "epdc_expert_gate_grad",
+           "epdc_int_quantize", "epdc_expert_gate_int", "epdc_expert_linear_int")
 # include/epdc.h: the dispatch scratch's status word (index in 32-bit words) and its values
 EPDC_STATUS_WORD = 2
 EPDC_STATUS_WAIT_TIMEOUT = 1
@@ -37,6 +39,7 @@ EPDC_MAX_SCALE_DIM = 1024
 EPDC_SOFTMAX, EPDC_SIGMOID = 0, 1
 EPDC_MAX_ROUTE_EXPERTS = 1024
 EPDC_MAX_GROUP_EXPERTS = 1024
+EPDC_MAX_EXPERT_DIM = 131056
 
 
 class EpdcError(RuntimeError):
@@ -128,6 +131,22 @@ def load_library() -> ctypes.CDLL:
     lib.epdc_group_experts.argtypes = [cfgp, i32] + [p] * 8 + [sz, p]
     lib.epdc_expert_product.restype = ctypes.c_int
     lib.epdc_expert_product.argtypes = [i32] * 5 + [p] * 8 + [i32, p]
+    lib.epdc_expert_linear.restype = ctypes.c_int
+    lib.epdc_expert_linear.argtypes = [i32] * 5 + [p] * 6 + [i32, p]
+    lib.epdc_expert_rows_grad.restype = ctypes.c_int
+    lib.epdc_expert_rows_grad.argtypes = [i32] * 5 + [p] * 6 + [i32, p]
+    lib.epdc_expert_weights_grad.restype = ctypes.c_int
+    lib.epdc_expert_weights_grad.argtypes = [i32] * 5 + [p] * 2 + [i32] + [p] * 5 + [i32, p]
+    lib.epdc_expert_gate.restype = ctypes.c_int
+    lib.epdc_expert_gate.argtypes = [i32] * 4 + [p] * 4 + [i32, p]
+    lib.epdc_expert_gate_grad.restype = ctypes.c_int
+    lib.epdc_expert_gate_grad.argtypes = [i32] * 4 + [p] * 4 + [i32] + [p] * 3
+    lib.epdc_int_quantize.restype = ctypes.c_int
+    lib.epdc_int_quantize.argtypes = [i32] * 4 + [p] * 5
+    lib.epdc_expert_gate_int.restype = ctypes.c_int
+    lib.epdc_expert_gate_int.argtypes = [i32] * 4 + [p] * 6
+    lib.epdc_expert_linear_int.restype = ctypes.c_int
+    lib.epdc_expert_linear_int.argtypes = [i32] * 5 + [p] * 8 + [i32, p]
     lib.epdc_last_error.restype = ctypes.c_char_p
     lib.epdc_last_error.argtypes = []
     _lib = lib

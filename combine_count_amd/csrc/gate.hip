@@ -1,0 +1,125 @@
+// The gated activation between an expert's two products, and its gradient, for
+// gfx950: a = w g s(g) u with s(g) = 1 / (1 + exp(-g)), g and u the two halves
+// of a row.
+//
+//   da/dg = w u s (1 + g (1 - s)),  da/du = w g s,  da/dw = g s u
+//
+// Both are bound by memory: every element is read and written once, eight of
+// them (16 bytes of bf16) by a lane at a time.  The forward pass goes over the
+// elements without regard to rows; the gradient sums a row's da/dw, so a wave
+// (short rows) or a block takes a row.
+#include "expert_elems.h"
+
+namespace epdc {
+namespace {
+
+constexpr int kUnits = 2;  // units of eight elements per thread of the forward pass
+
+template <bool FP32, bool OUT32>
+__global__ __launch_bounds__(256) void gate_kernel(GateParams P, DivMagic rowDiv) {
+    const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
+    const uint32_t perRow = P.F / 8;
+    const int64_t at = (int64_t)blockIdx.x * (256 * kUnits);
+    const int64_t blockRow = at / perRow;
+    const uint32_t blockUnit = (uint32_t)(at - blockRow * perRow);
+    if (blockRow >= rows.last) return;
+    Raw8<FP32> g[kUnits], u[kUnits];
+    int32_t row[kUnits], unit[kUnits];
+    float w[kUnits];
+    bool live[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const uint32_t n = blockUnit + i * 256 + threadIdx.x, r = div_by(n, rowDiv);
+        row[i] = (int32_t)min(blockRow + r, (int64_t)INT32_MAX);
+        unit[i] = (int32_t)(n - r * perRow);
+        live[i] = row[i] >= rows.first && row[i] < rows.last;
+        if (!live[i]) continue;
+        const uint8_t *h = P.h + (int64_t)row[i] * P.F * (FP32 ? 8 : 4);
+        g[i] = load_raw8<FP32>(h, unit[i]);
+        u[i] = load_raw8<FP32>(h, perRow + unit[i]);
+        w[i] = P.entryWeight ? P.entryWeight[row[i]] : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        if (!live[i]) continue;
+        const Eight gv = to_eight<FP32>(g[i]), uv = to_eight<FP32>(u[i]);
+        Eight a;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a.v[j] = gv.v[j] * sigmoid_of(gv.v[j]).s * uv.v[j] * w[i];
+        store_eight<OUT32>(P.out + (int64_t)row[i] * P.F * (OUT32 ? 4 : 2), unit[i], a);
+    }
+}
+
+template <bool FP32, bool OUT32, int TEAM>
+__global__ __launch_bounds__(256) void gate_grad_kernel(GateParams P) {
+    __shared__ float part[4];
+    const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
+    const int32_t row = (int32_t)(blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM);
+    if (row < rows.first || row >= rows.last) return;  // the whole team
+    const int32_t lane = threadIdx.x % TEAM, perRow = P.F / 8;
+    const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4), *d = P.dOut + (int64_t)row * P.F * (OUT32 ? 4 : 2);
+    uint8_t *out = P.out + (int64_t)row * P.F * (FP32 ? 8 : 4);
+    const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
+    float sum = 0.0f;
+    for (int32_t unit = lane; unit < perRow; unit += TEAM) {
+        const Raw8<FP32> graw = load_raw8<FP32>(h, unit), uraw = load_raw8<FP32>(h, perRow + unit);
+        const Raw8<OUT32> draw = load_raw8<OUT32>(d, unit);
+        const Eight g = to_eight<FP32>(graw), u = to_eight<FP32>(uraw), da = to_eight<OUT32>(draw);
+        Eight dg, du;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const Sigmoid s = sigmoid_of(g.v[j]);
+            const float gs = g.v[j] * s.s;
+            sum = fmaf(da.v[j] * gs, u.v[j], sum);
+            dg.v[j] = da.v[j] * w * u.v[j] * (s.s * fmaf(g.v[j], s.rest, 1.0f));
+            du.v[j] = da.v[j] * w * gs;
+        }
+        store_eight<FP32>(out, unit, dg);
+        store_eight<FP32>(out, perRow + unit, du);
+    }
+    if (!P.perEntry) return;
+    sum = team_sum<TEAM>(sum, part);
+    if (lane == 0) P.perEntry[row] = sum;
+}
+
+}  // namespace
+
+hipError_t launch_gate(const GateParams &P, bool fp32, bool out32, hipStream_t stream) {
+    const int64_t blocks = ((int64_t)P.maxEntries * (P.F / 8) + 256 * kUnits - 1) / (256 * kUnits);
+    if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+    const DivMagic div = div_magic((uint32_t)P.F / 8);
+    const dim3 grid((uint32_t)blocks);
+    if (fp32 && out32)
+        hipLaunchKernelGGL((gate_kernel<true, true>), grid, dim3(256), 0, stream, P, div);
+    else if (fp32)
+        hipLaunchKernelGGL((gate_kernel<true, false>), grid, dim3(256), 0, stream, P, div);
+    else if (out32)
+        hipLaunchKernelGGL((gate_kernel<false, true>), grid, dim3(256), 0, stream, P, div);
+    else
+        hipLaunchKernelGGL((gate_kernel<false, false>), grid, dim3(256), 0, stream, P, div);
+    return hipGetLastError();
+}
+
+namespace {
+
+template <int TEAM>
+hipError_t launch_gate_grad_team(const GateParams &P, bool fp32, bool out32, hipStream_t stream) {
+    const dim3 grid((uint32_t)ceil_div(P.maxEntries, 256 / TEAM));
+    if (fp32 && out32)
+        hipLaunchKernelGGL((gate_grad_kernel<true, true, TEAM>), grid, dim3(256), 0, stream, P);
+    else if (fp32)
+        hipLaunchKernelGGL((gate_grad_kernel<true, false, TEAM>), grid, dim3(256), 0, stream, P);
+    else if (out32)
+        hipLaunchKernelGGL((gate_grad_kernel<false, true, TEAM>), grid, dim3(256), 0, stream, P);
+    else
+        hipLaunchKernelGGL((gate_grad_kernel<false, false, TEAM>), grid, dim3(256), 0, stream, P);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gate_grad(const GateParams &P, bool fp32, bool out32, hipStream_t stream) {
+    return P.F <= 512 ? launch_gate_grad_team<64>(P, fp32, out32, stream) : launch_gate_grad_team<256>(P, fp32, out32, stream);
+}
+
+}  // namespace epdc

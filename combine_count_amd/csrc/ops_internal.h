@@ -1,7 +1,7 @@
 // Kernel parameters and launchers of the operators next to dispatch and
 // combine: routing (route.hip), fp4x2 quantisation (mx.hip), grouping by
-// expert (group.hip) and the experts' product (product.hip).  Not part of
-// the C ABI.
+// expert (group.hip), the experts' product (product.hip), and the experts in
+// bf16 and int8 (product_dense.hip, gate.hip, int8.hip).  Not part of the C ABI.
 #pragma once
 
 #include "epdc_internal.h"
@@ -149,6 +149,46 @@ inline ProductForm plan_product(int32_t E, int32_t N, int32_t H, int32_t maxEntr
     return mean >= 96 && tiles256 >= 512 ? kProductTiles256 : kProductTiles128;
 }
 
+// A product of bf16 or int8 rows and its gradients.
+struct DenseParams {
+    int32_t E, N, H;          // experts, output columns, elements per row
+    int32_t maxEntries;
+    int32_t numRows;          // of rows (the rows' gradient: of dOut)
+    int32_t numOutRows;       // of dOut (the weights' gradient)
+    const uint8_t *rows;      // [numRows][H] (the rows' gradient: dOut [numRows][N])
+    const float *rowScales;   // [numRows], int8
+    const int32_t *offsets;
+    const int32_t *entryRow;
+    const float *entryWeight;
+    const uint8_t *weights;   // [E][N][H]
+    const float *weightScales;  // [E][N], int8
+    const uint8_t *dOut;      // [numOutRows][N], the weights' gradient
+    const int32_t *outRow;
+    const uint8_t *base;      // [E][N][H] of the output's type, or NULL
+    uint8_t *out;
+};
+// out = rows . weights^T; dRows = dOut . weights; dWeights = dOut^T . rows
+enum DenseKind { kDenseProduct, kDenseRowsGrad, kDenseWeightsGrad };
+
+struct GateParams {
+    int32_t E, F, maxEntries;
+    const uint8_t *h;         // [maxEntries][2 F]
+    const int32_t *offsets;   // or NULL
+    const float *entryWeight;
+    const uint8_t *dOut;      // [maxEntries][F]
+    uint8_t *out;             // [maxEntries][F]; the gradient: dH [maxEntries][2 F]; int8 codes
+    float *perEntry;          // the gradient: dEntryWeight or NULL; int8: scales
+};
+
+struct Int8Params {
+    int32_t M, cols;          // rows per window
+    int64_t rows;
+    const int32_t *rowCount;
+    const uint8_t *x;
+    uint8_t *q;
+    float *scales;
+};
+
 template <int I>
 struct Const {
     static constexpr int value = I;
@@ -189,5 +229,10 @@ hipError_t launch_mx_dequantize(const MxParams &p, bool fp32, hipStream_t stream
 int64_t group_scratch_words(int32_t W, int32_t M, int32_t K, int32_t Epr);
 hipError_t launch_group(const GroupParams &p, hipStream_t stream);
 hipError_t launch_product(const ProductParams &p, bool out32, hipStream_t stream);
+hipError_t launch_dense(const DenseParams &p, DenseKind kind, bool int8, bool out32, hipStream_t stream);
+hipError_t launch_gate(const GateParams &p, bool fp32, bool out32, hipStream_t stream);
+hipError_t launch_gate_grad(const GateParams &p, bool fp32, bool out32, hipStream_t stream);
+hipError_t launch_gate_int(const GateParams &p, bool fp32, hipStream_t stream);
+hipError_t launch_int_quantize(const Int8Params &p, bool fp32, hipStream_t stream);
 
 }  // namespace epdc

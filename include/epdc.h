@@ -25,6 +25,11 @@
  *             fp4x2 wire's codes and scales, the expert-sorted list of a
  *             window's rows, and the product of those rows with each expert's
  *             fp4x2 weights.  Declared in the second half of this file.
+ *   the experts in bf16 and int8
+ *             The products of bf16 rows with their gradients, the gated
+ *             activation between an expert's two products with its gradient,
+ *             and the same forward path in int8 with a scale per token and
+ *             per column.  Declared at the end of this file.
  *
  * Argument names follow EpCfg (MORI JIT v2 design doc, §3.2).  The geometry
  * fields of EpCfg (blockNum, warpPerBlock, waveSize) are not part of the ABI:
@@ -503,6 +508,144 @@ int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, 
                         int32_t numRows, const void *rows, const void *rowScales, const int32_t *offsets,
                         const int32_t *entryRow, const float *entryWeight, const void *weights,
                         const void *weightScales, void *out, int32_t outDtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The experts in bf16, with their gradients
+ *
+ * Entries, groups and offsets as in epdc_expert_product: numExperts (1..65535)
+ * groups, group e holds entries [offsets[e], offsets[e+1]), values clamped to
+ * [0, maxEntries], a group ending at the smallest of the offsets behind its
+ * start's.  Rows of weights[e] are the expert's output columns.  Matrices are
+ * dense; rows, weights, gradients and outputs are 16-byte aligned, the other
+ * arrays 4-byte.  Products of bf16 values are summed in fp32, in an order that
+ * is fixed for given sizes (results are the same from run to run), and rounded
+ * once (nearest, ties to even).  maxEntries is best the number of entries that
+ * can occur: it chooses the kernel.
+ *
+ * The weight of an entry (its token's routing weight) can be applied once, in
+ * epdc_expert_gate: the second product then needs none, nor do its gradients,
+ * and epdc_expert_gate_grad gives the weight's gradient.
+ * ------------------------------------------------------------------------ */
+
+/* Largest hiddenDim of the calls below, and largest cols of an activation. */
+#define EPDC_MAX_EXPERT_DIM 131056
+
+/*
+ * out[i] = w_i * (rows[r_i] . weights[e]^T) for every entry i of every group e.
+ *
+ * rows [numRows][hiddenDim] bf16, weights [numExperts][numCols][hiddenDim]
+ * bf16, hiddenDim a multiple of 8.  entryRow, entryWeight, out [maxEntries]
+ * [numCols] of outDtype, numCols and what is left untouched as in
+ * epdc_expert_product.
+ */
+int epdc_expert_linear(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
+                             int32_t numRows, const void *rows, const int32_t *offsets, const int32_t *entryRow,
+                             const float *entryWeight, const void *weights, void *out, int32_t outDtype,
+                             void *stream);
+
+/*
+ * The gradient of the product's rows, one row per entry:
+ * dRows[i] = w_i * (dOut[r_i] . weights[e]).
+ *
+ * dOut [numRows][numCols] bf16, numCols a multiple of 8; entryRow is the row
+ * r_i of dOut (NULL: r_i = i; outside [0, numRows): a row of +0); weights as
+ * in the product, hiddenDim a multiple of 8; entryWeight [maxEntries] fp32 or
+ * NULL (1).  dRows [maxEntries][hiddenDim] of dtype (EPDC_BF16 or EPDC_FP32);
+ * rows outside the groups are left untouched.  Rows that several entries share
+ * have the sum of those entries' gradients: epdc_combine with
+ * epdc_group_experts' entryOf.
+ */
+int epdc_expert_rows_grad(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries, int32_t numRows,
+                          const void *dOut, const int32_t *offsets, const int32_t *entryRow, const float *entryWeight,
+                          const void *weights, void *dRows, int32_t dtype, void *stream);
+
+/*
+ * The gradient of the product's weights:
+ * dWeights[e] = base[e] + sum over group e's entries i of dOut[o_i]^T . rows[r_i].
+ *
+ * dOut [numOutRows][numCols] and rows [numRows][hiddenDim] bf16, numCols and
+ * hiddenDim multiples of 8.  outRow and entryRow [maxEntries] int32 (NULL:
+ * entry i's own index); an entry with either outside its array adds nothing.
+ * dWeights [numExperts][numCols][hiddenDim] of dtype (EPDC_BF16 or EPDC_FP32),
+ * every element written, of experts without an entry too.  base: NULL (0) or
+ * an array like dWeights, which may be dWeights itself (gradients that add
+ * up); it is added to the fp32 sum before the one rounding.
+ */
+int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
+                             int32_t numOutRows, const void *dOut, const int32_t *outRow, int32_t numRows,
+                             const void *rows, const int32_t *entryRow, const int32_t *offsets, const void *base,
+                             void *dWeights, int32_t dtype, void *stream);
+
+/*
+ * The gated activation between an expert's two products:
+ * out[i] = w_i * g * s(g) * u, s(g) = 1 / (1 + exp(-g)), elementwise.
+ *
+ * h [maxEntries][2 cols] of dtype (EPDC_BF16 or EPDC_FP32): g is the first
+ * half of a row, u the second (the columns of a first product whose weights
+ * hold the gate's rows, then the others).  cols: a multiple of 8 up to
+ * EPDC_MAX_EXPERT_DIM.  Rows i in [offsets[0], offsets[numExperts]) (clamped to
+ * [0, maxEntries]; offsets NULL: all) are read and written.  entryWeight
+ * [maxEntries] fp32 is w_i (NULL: 1).  out [maxEntries][cols] of outDtype.
+ * Computed in fp32 and rounded once.  NaN and infinities propagate as the
+ * formula's operations do (g = -inf gives NaN).
+ */
+int epdc_expert_gate(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
+                     const int32_t *offsets, const float *entryWeight, void *out, int32_t outDtype, void *stream);
+
+/*
+ * Its gradient, from dOut [maxEntries][cols] of outDtype: with s = s(g),
+ * dH [maxEntries][2 cols] of dtype holds w_i dOut u s (1 + g (1 - s)), then
+ * w_i dOut g s; dEntryWeight [maxEntries] fp32 (or NULL: not wanted) the sum of
+ * dOut g s u over a row, in an order that is fixed for given cols.  entryWeight NULL: 1.
+ */
+int epdc_expert_gate_grad(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
+                          const int32_t *offsets, const float *entryWeight, const void *dOut, int32_t outDtype,
+                          void *dH, float *dEntryWeight, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The experts in int8
+ *
+ * A quantised row is C int8 codes in [-127, 127] and one fp32 scale, a code
+ * being worth itself times the scale.  A dispatch carries such rows as
+ * EPDC_FP8 (one byte per element, moved as they are) with scaleDim 1.  The
+ * experts' weights are rows of the same kind, one scale per output column.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Quantise rows.  x [numWindows][rowsPerWindow][cols] of dtype (EPDC_BF16 or
+ * EPDC_FP32), cols a multiple of 16 up to EPDC_MAX_EXPERT_DIM; q [numWindows]
+ * [rowsPerWindow][cols] int8 (x and q 16-byte aligned), scales [numWindows]
+ * [rowsPerWindow] fp32.  rowCount as in epdc_mx_quantize.
+ * scale = m / 127, m the row's largest magnitude; a code is x / scale, rounded
+ * to the nearest integer, ties to even, and taken to at most 127 in magnitude
+ * (both quotients in fp32, rounded to nearest).  Where the scale comes out as 0
+ * the codes are 0.  A row that holds a NaN or an infinity gets scale NaN and
+ * codes 0.
+ */
+int epdc_int_quantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, int32_t dtype, const void *x,
+                       const int32_t *rowCount, void *q, float *scales, void *stream);
+
+/*
+ * epdc_expert_gate, quantised: the row's values w_i g s(g) u, each taken in 64
+ * bits and rounded to fp32, become q [maxEntries][cols] and scales
+ * [maxEntries] as in epdc_int_quantize.  cols is a multiple of 16.  (The codes
+ * are those of the 64-bit values, so they do not depend on how a 32-bit
+ * exponential rounds.)
+ */
+int epdc_expert_gate_int(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
+                          const int32_t *offsets, const float *entryWeight, void *q, float *scales, void *stream);
+
+/*
+ * epdc_expert_linear of int8 rows and weights:
+ * out[i][n] = w_i * (sum * rowScales[r_i] * weightScales[e][n]), sum the exact
+ * 32-bit integer rows[r_i] . weights[e][n], then fp32 products from the left
+ * (w_i last) and one rounding.  hiddenDim is a multiple of 16; rowScales
+ * [numRows], weightScales [numExperts][numCols] fp32.  Codes may be any int8.
+ */
+int epdc_expert_linear_int(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
+                             int32_t numRows, const void *rows, const float *rowScales, const int32_t *offsets,
+                             const int32_t *entryRow, const float *entryWeight, const void *weights,
+                             const float *weightScales, void *out, int32_t outDtype, void *stream);
 
 /* Message for the last failing call on this thread ("" if none).  The
  * pointer stays valid until the next epdc_* call on the same thread.  MORI
