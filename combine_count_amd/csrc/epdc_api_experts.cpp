@@ -55,7 +55,8 @@ int product_params(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32
     P.H = hiddenDim;
     P.maxEntries = maxEntries;
     P.numRows = numRows;
-    P.rows = static_cast<const uint8_t *>(rows);
+    // with no rows every entry is a row of zeros; what is loaded in its place are weights
+    P.rows = static_cast<const uint8_t *>(numRows > 0 ? rows : weights);
     P.offsets = offsets;
     P.entryRow = entryRow;
     P.entryWeight = entryWeight;

@@ -170,6 +170,18 @@ struct DenseParams {
 // out = rows . weights^T; dRows = dOut . weights; dWeights = dOut^T . rows
 enum DenseKind { kDenseProduct, kDenseRowsGrad, kDenseWeightsGrad };
 
+// Their kernels: tiles of 128 x 128 or 256 x 256 of the output.
+enum DenseForm { kDenseTiles128, kDenseTiles256 };
+
+inline DenseForm plan_dense(DenseKind kind, int32_t E, int32_t N, int32_t H, int32_t maxEntries) {
+    const int32_t columns = kind == kDenseProduct ? N : H;
+    if (kind == kDenseWeightsGrad)
+        return (int64_t)E * ceil_div(N, 256) * ceil_div(H, 256) >= 256 ? kDenseTiles256 : kDenseTiles128;
+    const int64_t groups = E < maxEntries ? E : maxEntries;
+    const int64_t tiles256 = (maxEntries / 256 + groups / 2) * ceil_div(columns, 256);
+    return ceil_div(maxEntries, E) >= 96 && tiles256 >= 512 ? kDenseTiles256 : kDenseTiles128;
+}
+
 struct GateParams {
     int32_t E, F, maxEntries;
     const uint8_t *h;         // [maxEntries][2 F]
