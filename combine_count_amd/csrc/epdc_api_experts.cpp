@@ -151,13 +151,15 @@ int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hidden
         P.E = numExperts;
         P.N = numCols;
         P.H = hiddenDim;
-        P.maxEntries = maxEntries;
+        // with no rows on a side no entry is one; what is loaded in their place is of the output
+        const bool none = numRows == 0 || numOutRows == 0;
+        P.maxEntries = none ? 0 : maxEntries;
         P.numRows = numRows;
         P.numOutRows = numOutRows;
-        P.rows = static_cast<const uint8_t *>(rows);
+        P.rows = static_cast<const uint8_t *>(none ? dWeights : rows);
         P.offsets = offsets;
         P.entryRow = entryRow;
-        P.dOut = static_cast<const uint8_t *>(dOut);
+        P.dOut = static_cast<const uint8_t *>(none ? dWeights : dOut);
         P.outRow = outRow;
         P.base = static_cast<const uint8_t *>(base);
         P.out = static_cast<uint8_t *>(dWeights);

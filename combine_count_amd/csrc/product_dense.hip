@@ -11,20 +11,50 @@
 namespace epdc {
 namespace {
 
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_dword __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at 4-byte alignment
 
-// The sums of 32 x 32 products stay in accumulation registers that the matrix
-// instruction updates in place, in the order written.  The compiler does not
-// see the instruction: its operands must not come from a vector instruction
-// just before it, and its sums are read behind mfma_done().
-__device__ __forceinline__ void mfma_inplace(f32x16 &c, u32x4 a, u32x4 b) {
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+// The sums of 32 x 32 products stay in accumulation registers of their own,
+// named here (fragment f: a16f .. a16f + 15) and marked as overwritten by every
+// statement that touches them, so that the compiler keeps nothing there: its own
+// allocation of 256 of them moved them about or spilled where the kernel has
+// several bodies.  It does not see the matrix instruction: its operands must not
+// come from a vector instruction just before it, and its sums are read behind
+// mfma_done().
+#define EPDC_A8(n) "a" #n "0", "a" #n "1", "a" #n "2", "a" #n "3", "a" #n "4", "a" #n "5", "a" #n "6", "a" #n "7", "a" #n "8", "a" #n "9"
+#define EPDC_SUMS64 \
+    "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", EPDC_A8(1), EPDC_A8(2), EPDC_A8(3), EPDC_A8(4), EPDC_A8(5), "a60", "a61", "a62", "a63"
+#define EPDC_SUMS256 \
+    EPDC_SUMS64, "a64", "a65", "a66", "a67", "a68", "a69", EPDC_A8(7), EPDC_A8(8), EPDC_A8(9), EPDC_A8(10), EPDC_A8(11), EPDC_A8(12), EPDC_A8(13), \
+        EPDC_A8(14), EPDC_A8(15), EPDC_A8(16), EPDC_A8(17), EPDC_A8(18), EPDC_A8(19), EPDC_A8(20), EPDC_A8(21), EPDC_A8(22), EPDC_A8(23), EPDC_A8(24), \
+        "a250", "a251", "a252", "a253", "a254", "a255"
+#define EPDC_MFMA(NAME, SUMS)                                                                                                     \
+    if constexpr (FIRST)                                                                                                          \
+        asm volatile(NAME " a[%2:%3], %0, %1, 0" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15) : SUMS);                       \
+    else                                                                                                                          \
+        asm volatile(NAME " a[%2:%3], %0, %1, a[%2:%3]" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15) : SUMS);
+// Fragment F of a wave's ALL (4 or 16): += a . b, or with FIRST = a . b.
+template <int F, int ALL, bool FIRST, bool INT8>
+__device__ __forceinline__ void mfma_sums(u32x4 a, u32x4 b) {
+    if constexpr (INT8 && ALL == 16) {
+        EPDC_MFMA("v_mfma_i32_32x32x32_i8", EPDC_SUMS256)
+    } else if constexpr (INT8) {
+        EPDC_MFMA("v_mfma_i32_32x32x32_i8", EPDC_SUMS64)
+    } else if constexpr (ALL == 16) {
+        EPDC_MFMA("v_mfma_f32_32x32x16_bf16", EPDC_SUMS256)
+    } else {
+        EPDC_MFMA("v_mfma_f32_32x32x16_bf16", EPDC_SUMS64)
+    }
 }
-__device__ __forceinline__ void mfma_inplace(i32x16 &c, u32x4 a, u32x4 b) {
-    asm volatile("v_mfma_i32_32x32x32_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+// Sum V of fragment F, as it lies in the register.
+template <int F, int ALL, int V>
+__device__ __forceinline__ uint32_t read_sum() {
+    uint32_t x;
+    if constexpr (ALL == 16)
+        asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(F * 16 + V) : EPDC_SUMS256);
+    else
+        asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(F * 16 + V) : EPDC_SUMS64);
+    return x;
 }
 
 // Four bf16 of a column of a 4 x 16 block in LDS (rows of the block 8 bytes at
@@ -61,29 +91,39 @@ __device__ __forceinline__ void load_lds4_unseen(const int32_t *src, uint32_t ld
 
 __device__ u32x4 zero_piece;  // what is loaded in place of pieces that do not exist; never written
 
+// For the compiler: code of a tile's ends lies outside the loop over its steps.
+__device__ __forceinline__ bool rarely(bool b) { return __builtin_expect(b, 0); }
+
 // Where a tile of the output lies: expert, entries [lo, hi) of its group (of
 // the tile, but for the weights' gradient), rows from r0, columns from c0.
 struct DenseTile {
     int32_t e, lo, hi, r0, c0;
 };
 
-// A BM x BN tile of the output by four waves, (BM/2) x (BN/2) each, in 32 x 32
-// fragments; the output's columns are the instruction's rows and its rows the
-// instruction's columns, so a lane ends with runs of 8 consecutive columns of
-// one row.
+// A BM x BN tile of the output by four waves, half its columns and every other
+// 32 of its rows each, in 32 x 32 fragments; the output's columns are the
+// instruction's rows and its rows the instruction's columns, so a lane ends with
+// runs of 8 consecutive columns of one row.  A tile of fewer rows takes the
+// fragments that hold them only, and a group's rows are dealt out evenly over
+// its tiles, 64 by 64 (1024 entries of an expert on average: an eighth of the
+// products of whole tiles would be of rows that do not exist).
 //
 // The summed index goes in steps of 128 bytes of it (64 bf16, 128 int8) through
-// two pairs of LDS buffers, loaded by the memory pipeline itself.  A step is
+// two pairs of places in LDS, loaded by the memory pipeline itself.  A step is
 // two halves; the operands of a half are read into registers during the half
 // before:
-//     read half 1 of step k        | products of half 0
+//     products of half 0 | read half 1 of step k
 //     wait: step k+1 has arrived (requested one whole step ago); barrier
-//     request step k+2 into step k's buffers
-//     read half 0 of step k+1      | products of half 1
+//     products of half 1 | request step k+2 into step k's places,
+//                        | read half 0 of step k+1
+// (Into the registers of products just issued instead, every read waits for
+// them: a fifth slower.  A fifth place, for the rows of step k+3: no gain.)
 // The steps of a block's tiles follow one another without a gap: behind a
 // tile's last step come the next tile's first (a stride of the grid further),
 // requested while the last ones are computed; a tile's results are stored with
-// them under way.  A tile has two steps at least (of zeros, if need be).
+// them under way.  A tile has two steps at least (of zeros, if need be).  What a
+// tile's begin and end need lies outside the loop over its steps: with it in
+// between, the loop's instructions come late (a quarter slower).
 //
 // An operand whose summed index runs along its rows in memory lies in LDS in
 // rows of 128 bytes, their 16-byte pieces at piece ^ row / 2 % 8, so that the 16
@@ -94,20 +134,33 @@ struct DenseTile {
 // index, so that the eight rows of a read spread over the banks.
 template <DenseKind KIND, bool INT8, int BM, int BN, bool OUT32>
 __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_kernel(DenseParams P) {
-    using Acc = std::conditional_t<INT8, i32x16, f32x16>;
     constexpr bool kTurnedC = KIND != kDenseProduct, kTurnedR = KIND == kDenseWeightsGrad;
     constexpr int ES = INT8 ? 1 : 2;            // bytes of an element
     constexpr int FR = BM / 64, FC = BN / 64;   // fragments of a wave
     constexpr int LR = BM / 32, LC = BN / 32;   // LDS loads of a wave per step (1 KB each)
-    __shared__ __attribute__((aligned(16))) uint8_t rbuf0[BM * 128], rbuf1[BM * 128], cbuf0[BN * 128], cbuf1[BN * 128];
+    static_assert(BM == BN, "the places in LDS hold either operand");
+    constexpr int kPlace = BM * 128;
+    __shared__ __attribute__((aligned(16))) uint8_t ring[4 * kPlace];  // rows and columns of a step, those of the next
     // The weights' gradient: rows of a step's entries (of dOut, of rows), of four steps that follow one another.
     __shared__ int32_t list[4][2][64];
+    // The others: of the rows of this tile and the next, the entry's weight, its scale, and whether it has a row.
+    struct RowInfo {
+        float factor, scale;
+        int32_t there;
+    };
+    __shared__ RowInfo rowInfo[KIND == kDenseWeightsGrad ? 1 : 2][KIND == kDenseWeightsGrad ? 1 : BM];
     const int32_t C = KIND == kDenseProduct ? P.N : P.H;  // the output's columns
     const int32_t RT = ceil_div(P.N, BM), CT = ceil_div(C, BN);
     const int32_t rowOut = C * (OUT32 ? 4 : 2);
     const int32_t kBytes = KIND == kDenseProduct ? P.H * ES : P.N * ES;  // of a row of the summed index (not the weights' gradient)
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int wr = (wave & 1) * (BM / 2), wc = (wave >> 1) * (BN / 2);
+    const int wr = (wave & 1) * 32, wc = (wave >> 1) * (BN / 2);  // its fragments' rows from wr, 64 apart
+    // The lane again, opaque: what is computed from it is computed there, not kept in registers from tile to tile.
+    auto fresh = [&] {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
     const uint8_t *const zero = reinterpret_cast<const uint8_t *>(&zero_piece);
 
     // ---- tiles
@@ -139,8 +192,11 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
             t = DenseTile{uniform(e), __builtin_amdgcn_readlane(groups.lo, e & 63), __builtin_amdgcn_readlane(groups.hi, e & 63),
                           uniform((band * size + r - c * rows) * BM), uniform(c * BN)};
         } else {
-            const TileAt a = find_tile<BM, BN>(P, groups, CT, b);
-            t = DenseTile{a.e, a.m0, a.hi, a.m0, a.n0};
+            const PlaceOf a = find_place<BM, BN>(P, groups, CT, b);
+            if (a.e < 0) return t;
+            const int64_t pairs = ceil_div((int64_t)a.hi - a.lo, 64);  // of fragments of the group, dealt out over its tiles
+            const int32_t first = (int32_t)(pairs * a.m / a.tiles), end = (int32_t)(pairs * (a.m + 1) / a.tiles);
+            t = DenseTile{a.e, a.lo + first * 64, (int32_t)min((int64_t)a.hi, a.lo + (int64_t)end * 64), 0, a.n0};
         }
         return DenseTile{uniform(t.e), uniform(t.lo), uniform(t.hi), uniform(t.r0), uniform(t.c0)};
     };
@@ -156,32 +212,43 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
     DenseTile next = find(b), Q{-1, 0, 0, 0, 0};
     if (next.e < 0) return;
     int32_t kq = 0, stepsQ = 0;
-    // Rows along the summed index: where this lane's rows begin in the rows' array, their offsets from the tile's first
-    // column, and the place in a row (of even and odd loads) that it requests.
-    const uint8_t *rowp[kTurnedR ? 1 : LR];
+    // Rows along the summed index: this lane's rows, its columns' offsets from the tile's first, and the place in a row
+    // (of even and odd loads) that it requests.
+    uint32_t rowi[kTurnedR ? 1 : LR];
     uint32_t colo[kTurnedC ? 1 : LC];
     const int piece = ((lane & 7) ^ (lane >> 4)) * 16;  // of a step, in even loads (in odd ones ^ 64)
-    uint32_t place[2] = {0, 0};
+    const uint8_t *placeR[2] = {nullptr, nullptr};
+    uint32_t placeC[2] = {0, 0};
     const uint8_t *stepBase = nullptr;  // columns that are not gathered: from where this step's are requested
-    int32_t entryRow = -1;  // the row of entry wave * (BM/4) + lane of the next tile, on its way
+    // Of entry wave * (BM/4) + lane: row and weight in the next tile, on their way, and what is known of it in tile Q.
+    int32_t entryRow = -1;
+    float entryWeight = 1.0f;
+    RowInfo infoQ{};
     // Turned rows: lanes of a row of BX elements, rows of a load, and the 16-byte piece that this lane requests.
     constexpr int kLanesR = BM / 8, kPerR = 64 / kLanesR, kLanesC = BN / 8, kPerC = 64 / kLanesC;
-    uint32_t turnedR[kTurnedR ? (BM == 256 ? 4 : 1) : 1], turnedC[kTurnedC ? (BN == 256 ? 4 : 1) : 1];
+    constexpr int kSwR = BM == 256 ? 4 : 1, kSwC = BN == 256 ? 4 : 1;  // swizzles of a wave's loads
+    uint32_t turnedC[kTurnedC ? kSwC : 1];
+    const uint8_t *fromR[kTurnedR ? kSwR : 1], *fromC[kTurnedR ? kSwC : 1];  // gathered: of row 0
+    const uint8_t *src[kTurnedR ? LR + LC : 1];                             // and of the step's rows
     // offset of the piece in the tile's part of a row, by the load's swizzle; behind the row's end the last piece
     auto turned_piece = [&](auto bx, int s, int32_t left) {
         constexpr int BX = decltype(bx)::value;
-        const int p = lane & (BX / 8 - 1);
-        const int sw = BX == 256 ? ((s & 1) * 2 + (lane >> 5)) | (s >> 1) << 2 : lane >> 4;
+        const int ln = fresh(), p = ln & (BX / 8 - 1);
+        const int sw = BX == 256 ? ((s & 1) * 2 + (ln >> 5)) | (s >> 1) << 2 : ln >> 4;
         return (uint32_t)min((p ^ (sw << 2)) * 16, left * 2 - 16);
     };
-    int32_t listR = 0, listC = 0;  // the weights' gradient: rows of entry wave * 16 + lane % 16 of the next step, as listed
-    int32_t idxR = -1, idxC = -1;  // and of the step that is requested; -1: none
-    uint32_t slot = 0;             // of that step among all, % 4 its lists' place
-    const uint8_t *colBase = nullptr, *rowBase = nullptr;
+    int32_t listR = 0, listC = 0;  // the weights' gradient: rows of entry `lane` of the next step, as listed
+    int32_t idxR = 0, idxC = 0;    // and of the step that is requested
+    uint64_t dead = 0;             // its entries that are none
+    uint32_t slot = 0;             // its place among all steps, % 4 its lists' place
+    const uint8_t *colBase = nullptr;
     auto fetch_entry = [&](const DenseTile &t) {  // product, rows' gradient
-        const int32_t ent = t.lo + wave * (BM / 4) + (lane & (BM / 4 - 1));
+        const int32_t ent = t.lo + wave * (BM / 4) + (fresh() & (BM / 4 - 1));
         entryRow = -1;
-        if (t.e >= 0 && ent < t.hi) entryRow = P.entryRow ? P.entryRow[ent] : ent;
+        if (t.e >= 0 && ent < t.hi) {
+            entryRow = P.entryRow ? P.entryRow[ent] : ent;
+            if (P.entryWeight) entryWeight = P.entryWeight[ent];
+        }
     };
     // Weights' gradient: the lists of step k of a tile, on their way into a place; wave 0 asks for dOut's, wave 1 for rows'.
     auto request_lists = [&](const DenseTile &t, int32_t k, uint32_t place) {
@@ -191,12 +258,19 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
         if (at < t.hi - t.lo) load_lds4_unseen(from + t.lo + at, lds_address(list[place & 3][wave]));
     };
     auto read_lists = [&](uint32_t place) {
-        if (P.outRow) listR = list[place & 3][0][wave * 16 + (lane & 15)];
-        if (P.entryRow) listC = list[place & 3][1][wave * 16 + (lane & 15)];
+        if (P.outRow) listR = list[place & 3][0][lane];
+        if (P.entryRow) listC = list[place & 3][1][lane];
     };
-    // Tile Q becomes `next`, or stays where there is none: what is requested then is not used.
+    // Tile Q becomes `next`, or stays where there is none: what is requested then is not used.  What is known of Q's
+    // rows, now the tile that is computed, goes to LDS.
+    int turns = 0;
     auto turn_to_next = [&] {
         kq = 0;
+        if constexpr (KIND != kDenseWeightsGrad) {
+            const int row = wave * (BM / 4) + fresh();
+            if (row < (wave + 1) * (BM / 4)) rowInfo[turns & 1][row] = infoQ;
+        }
+        ++turns;
         if (next.e < 0) {
             Q.e = -1;
             stepsQ = INT32_MAX;
@@ -205,98 +279,121 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
         Q = next;
         stepsQ = steps_of(Q);
         if constexpr (KIND != kDenseWeightsGrad) {
-            const int32_t row = (uint32_t)entryRow < (uint32_t)P.numRows ? entryRow : 0;  // an entry without a row: any row, and zeros stored
+            const int ln = fresh();
+            const bool there = (uint32_t)entryRow < (uint32_t)P.numRows;
+            const int32_t row = there ? entryRow : 0;  // an entry without a row: any row, and zeros stored
 #pragma unroll
-            for (int i = 0; i < LR; ++i) rowp[i] = P.rows + (int64_t)__shfl(row, i * 8 + (lane >> 3)) * kBytes;
+            for (int i = 0; i < LR; ++i) rowi[i] = (uint32_t)__shfl(row, i * 8 + (ln >> 3));
+            infoQ = RowInfo{entryWeight, 0.0f, there};
+            if constexpr (INT8) {
+                if (there) infoQ.scale = P.rowScales[row];
+            }
         }
         if constexpr (KIND == kDenseProduct) {
+            const int ln = fresh();
             colBase = P.weights + ((int64_t)Q.e * P.N + Q.c0) * kBytes;
 #pragma unroll
-            for (int i = 0; i < LC; ++i) colo[i] = (uint32_t)(min(wave * (BN / 4) + i * 8 + (lane >> 3), P.N - 1 - Q.c0) * kBytes);
+            for (int i = 0; i < LC; ++i) colo[i] = (uint32_t)(min(wave * (BN / 4) + i * 8 + (ln >> 3), P.N - 1 - Q.c0) * kBytes);
         } else {
             colBase = (KIND == kDenseRowsGrad ? P.weights + (int64_t)Q.e * P.N * P.H * 2 : P.rows) + (int64_t)Q.c0 * 2;
 #pragma unroll
-            for (int s = 0; s < (BN == 256 ? 4 : 1); ++s) {
+            for (int s = 0; s < kSwC; ++s) {
                 turnedC[s] = turned_piece(Const<BN>{}, s, P.H - Q.c0);
                 if constexpr (KIND == kDenseRowsGrad) turnedC[s] += (lane / kLanesC) * ((uint32_t)P.H * 2);
+                if constexpr (kTurnedR) fromC[s] = colBase + turnedC[s];
             }
-            if constexpr (kTurnedR) {
-                rowBase = P.dOut + (int64_t)Q.r0 * 2;
+        }
+        if constexpr (kTurnedR) {
 #pragma unroll
-                for (int s = 0; s < (BM == 256 ? 4 : 1); ++s) turnedR[s] = turned_piece(Const<BM>{}, s, P.N - Q.r0);
-            }
+            for (int s = 0; s < kSwR; ++s) fromR[s] = P.dOut + (int64_t)Q.r0 * 2 + turned_piece(Const<BM>{}, s, P.N - Q.r0);
         }
         b += gridDim.x;
         next = find(b);
         if constexpr (KIND != kDenseWeightsGrad) fetch_entry(next);
     };
-    // Step kq of tile Q, or the first of the next: what its requests need.
+    // What the requests of step kq of tile Q need.
     auto advance = [&] {
-        if (kq == stepsQ) turn_to_next();
-        const int32_t k = uniform(kq);
+        const int32_t k = uniform(min(kq, 1 << 22));
         if constexpr (KIND != kDenseWeightsGrad) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) place[i] = (uint32_t)min(min(k, 1 << 22) * 128 + (piece ^ i * 64), kBytes - 16);
+            for (int i = 0; i < 2; ++i) {
+                placeR[i] = P.rows + min(k * 128 + (piece ^ i * 64), kBytes - 16);
+                placeC[i] = (uint32_t)min(k * 128 + (piece ^ i * 64), kBytes - 16);
+            }
         }
         if constexpr (KIND == kDenseProduct) stepBase = uniform_pointer(colBase);
-        if constexpr (KIND == kDenseRowsGrad) stepBase = uniform_pointer(colBase + (int64_t)(min(k, 1 << 22) * 64 + wave * 16) * ((uint32_t)P.H * 2));
+        if constexpr (KIND == kDenseRowsGrad) stepBase = uniform_pointer(colBase + (int64_t)(k * 64 + wave * 16) * ((uint32_t)P.H * 2));
         if constexpr (KIND == kDenseWeightsGrad) {
-            const int32_t at = k * 64 + wave * 16 + (lane & 15);
+            const int32_t at = k * 64 + lane;
             const int32_t r = P.outRow ? listR : Q.lo + at, c = P.entryRow ? listC : Q.lo + at;
             const bool in = Q.e >= 0 && at < Q.hi - Q.lo && (uint32_t)r < (uint32_t)P.numOutRows && (uint32_t)c < (uint32_t)P.numRows;
-            idxR = in ? r : -1;
-            idxC = in ? c : -1;
-            if (k + 2 < stepsQ)
-                request_lists(Q, k + 2, slot + 2);
+            dead = ~__ballot(in);
+            idxR = in ? r : 0;
+            idxC = in ? c : 0;
+        }
+    };
+    // The lists of the steps behind it, once all waves' requests of before have arrived.
+    auto advance_lists = [&] {
+        if constexpr (KIND == kDenseWeightsGrad) {
+            if (kq + 2 < stepsQ)
+                request_lists(Q, kq + 2, slot + 2);
             else
-                request_lists(next, k + 2 - stepsQ, slot + 2);
+                request_lists(next, kq + 2 - stepsQ, slot + 2);
             read_lists(slot + 1);
             ++slot;
         }
     };
-    // The row's index of a turned load's lanes, from the lanes that hold them.
-    auto spread = [&](auto per, int32_t idx, int i) {
-        constexpr int kPer = decltype(per)::value;
-        int32_t v = __builtin_amdgcn_readlane(idx, i * kPer);
-#pragma unroll
-        for (int q = 1; q < kPer; ++q) v = lane / (64 / kPer) == q ? __builtin_amdgcn_readlane(idx, i * kPer + q) : v;
-        return v;
+    // Gathered: the place of load t of the wave's LR + LC.
+    auto prepare = [&](auto t) {
+        constexpr int T = decltype(t)::value, I = T < LR ? T : T - LR, kPer = T < LR ? kPerR : kPerC, BX = T < LR ? BM : BN;
+        constexpr int S = BX == 256 ? (I & 1) | (I >> 2) << 1 : 0;
+        const uint32_t r = (uint32_t)__builtin_amdgcn_ds_bpermute((wave * 16 + lane / (64 / kPer) + I * kPer) * 4, T < LR ? idxR : idxC);
+        src[T] = (T < LR ? fromR[S] : fromC[S]) + (uint64_t)r * (uint32_t)((T < LR ? P.N : P.H) * 2);
     };
-    // Load t of the wave's LR + LC of the step, into its places in LDS from rb and cb.
-    const uint32_t rto0 = lds_address(rbuf0 + wave * (BM / 4) * 128), rto1 = lds_address(rbuf1 + wave * (BM / 4) * 128);
-    const uint32_t cto0 = lds_address(cbuf0 + wave * (BN / 4) * 128), cto1 = lds_address(cbuf1 + wave * (BN / 4) * 128);
-    auto request = [&](auto t, uint32_t rb, uint32_t cb) {
-        constexpr int T = decltype(t)::value, I = T < LR ? T : T - LR, BX = T < LR ? BM : BN, S = BX == 256 ? (I & 1) | (I >> 2) << 1 : 0;
+    auto prepare_dead = [&] {  // of entries that are none, and behind the group's last: zeros
+        if (!rarely(dead != 0)) return;
+        const int ln = fresh();
+#pragma unroll
+        for (int t = 0; t < LR + LC; ++t) {
+            const int kPer = t < LR ? kPerR : kPerC, i = t < LR ? t : t - LR;
+            if (dead >> (wave * 16 + ln / (64 / kPer) + i * kPer) & 1) src[t] = zero;
+        }
+    };
+    // Load t of the wave's LR + LC of the step (rows, then columns), into its part of a place in LDS.
+    const uint32_t ringAt = lds_address(ring) + wave * (kPlace / 4);
+    auto request = [&](auto t, uint32_t place) {
+        constexpr int T = decltype(t)::value, I = T < LR ? T : T - LR;
+        const uint32_t to = ringAt + place;
         if constexpr (KIND == kDenseWeightsGrad) {
-            const int32_t r = T < LR ? spread(Const<kPerR>{}, idxR, I) : spread(Const<kPerC>{}, idxC, I);
-            const uint8_t *from = T < LR ? rowBase : colBase;
-            const uint64_t off = (uint64_t)(uint32_t)r * ((uint32_t)(T < LR ? P.N : P.H) * 2) + (T < LR ? turnedR[S] : turnedC[S]);
-            load_lds16_unseen<I * 1024>(r < 0 ? zero : from + off, T < LR ? rb : cb);
+            load_lds16_unseen<I * 1024>(src[T], to);
         } else if constexpr (T < LR) {
-            load_lds16_unseen<I * 1024>(rowp[I] + place[I & 1], rb);
+            load_lds16_unseen<I * 1024>(placeR[I & 1] + (uint64_t)rowi[I] * (uint32_t)kBytes, to);
         } else if constexpr (KIND == kDenseProduct) {
-            load_lds16_unseen<I * 1024>(stepBase, colo[I] + place[I & 1], cb);
+            load_lds16_unseen<I * 1024>(stepBase, colo[I] + placeC[I & 1], to);
         } else {
-            const int32_t left = P.N - 1 - uniform(kq) * 64 - wave * 16 - I * kPerC;  // rows behind the load's first
-            if (left >= kPerC - 1)
-                load_lds16_unseen<I * 1024>(uniform_pointer(stepBase + (int64_t)(I * kPerC) * ((uint32_t)P.H * 2)), turnedC[S], cb);
+            constexpr int S = BN == 256 ? (I & 1) | (I >> 2) << 1 : 0;
+            const int32_t left = P.N - 1 - uniform(min(kq, 1 << 22)) * 64 - wave * 16 - I * kPerC;  // rows behind the load's first
+            if (!rarely(left < kPerC - 1))
+                load_lds16_unseen<I * 1024>(uniform_pointer(stepBase + (int64_t)(I * kPerC) * ((uint32_t)P.H * 2)), turnedC[S], to);
             else  // the last row, where this lane's is behind it
-                load_lds16_unseen<I * 1024>(stepBase + ((int64_t)(I * kPerC) + min(left - lane / kLanesC, 0)) * ((uint32_t)P.H * 2) + turnedC[S], cb);
+                load_lds16_unseen<I * 1024>(stepBase + ((int64_t)(I * kPerC) + min(left - lane / kLanesC, 0)) * ((uint32_t)P.H * 2) + turnedC[S], to);
         }
     };
     // A step that has arrived, with places behind the end of the summed index (step k of its tile): zeros there, on
     // both sides, so that no value that is not part of the sum is multiplied.  (The weights' gradient loads them.)
-    auto clear_tail = [&](int32_t k, uint8_t *rb, uint8_t *cb) {
+    auto clear_tail = [&](int32_t k, uint32_t at) {
         if constexpr (KIND == kDenseWeightsGrad) return;
-        if ((k + 1) * 128 <= kBytes) return;
+        if (!rarely((k + 1) * 128 > kBytes)) return;
         const u32x4 none = {0, 0, 0, 0};
+        const int ln = fresh(), pc = ((ln & 7) ^ (ln >> 4)) * 16;
+        uint8_t *const rb = ring + at, *const cb = rb + kPlace;
 #pragma unroll
         for (int i = 0; i < LR; ++i)
-            if (k * 128 + (piece ^ (i & 1) * 64) >= kBytes) *reinterpret_cast<u32x4 *>(rb + wave * (BM / 4) * 128 + i * 1024 + lane * 16) = none;
+            if (k * 128 + (pc ^ (i & 1) * 64) >= kBytes) *reinterpret_cast<u32x4 *>(rb + wave * (BM / 4) * 128 + i * 1024 + ln * 16) = none;
 #pragma unroll
         for (int i = 0; i < LC; ++i) {
-            const bool behind = kTurnedC ? k * 64 + wave * 16 + i * kPerC + lane / kLanesC >= P.N : k * 128 + (piece ^ (i & 1) * 64) >= kBytes;
-            if (behind) *reinterpret_cast<u32x4 *>(cb + wave * (BN / 4) * 128 + i * 1024 + lane * 16) = none;
+            const bool behind = kTurnedC ? k * 64 + wave * 16 + i * kPerC + ln / kLanesC >= P.N : k * 128 + (pc ^ (i & 1) * 64) >= kBytes;
+            if (behind) *reinterpret_cast<u32x4 *>(cb + wave * (BN / 4) * 128 + i * 1024 + ln * 16) = none;
         }
         __syncthreads();
     };
@@ -321,51 +418,28 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
     }
     if constexpr (kTurnedR) {
 #pragma unroll
-        for (int f = 0; f < FR; ++f) turnR[f] = turnRowR + ((wr / 32 + f) ^ swR) * 64;
+        for (int f = 0; f < FR; ++f) turnR[f] = turnRowR + ((2 * f + (wave & 1)) ^ swR) * 64;
     }
-    constexpr int kReadsC = FC * 2 * (kTurnedC ? 2 : 1), kReadsR = FR * 2 * (kTurnedR ? 2 : 1), kReads = kReadsC + kReadsR;
-    // LDS read n of half `half` of a step: those of the first 32 bytes of the summed index first.
-    auto read = [&](auto n, Half &h, const uint8_t *rb, const uint8_t *cb, int half) {
-        constexpr int Nn = decltype(n)::value, CH = Nn >= kReads / 2, M = Nn - CH * (kReads / 2);
-        if constexpr (M < kReadsC / 2) {
-            if constexpr (kTurnedC) {
-                constexpr int F = M / 2, X = M % 2;
-                const u32x2 v = read_turned(cb + turnC[F] + (half * 32 + CH * 16 + X * 4) * (BN * 2));
-                h.c[F][CH][2 * X] = v.x;
-                h.c[F][CH][2 * X + 1] = v.y;
-            } else {
-                h.c[M][CH] = *reinterpret_cast<const u32x4 *>(cb + (alongC ^ (half * 64 + CH * 32)) + M * 4096);
-            }
+    // The LDS reads of fragment F, chunk CH (32 bytes of the summed index) of half `half` of a step.
+    auto read_r = [&](auto f, auto ch, Half &h, const uint8_t *rb, int half) {
+        constexpr int F = decltype(f)::value, CH = decltype(ch)::value;
+        if constexpr (kTurnedR) {
+            const u32x2 lo = read_turned(rb + turnR[F] + (half * 32 + CH * 16) * (BM * 2));
+            const u32x2 hi = read_turned(rb + turnR[F] + (half * 32 + CH * 16 + 4) * (BM * 2));
+            h.r[F][CH] = u32x4{lo.x, lo.y, hi.x, hi.y};
         } else {
-            constexpr int MR = M - kReadsC / 2;
-            if constexpr (kTurnedR) {
-                constexpr int F = MR / 2, X = MR % 2;
-                const u32x2 v = read_turned(rb + turnR[F] + (half * 32 + CH * 16 + X * 4) * (BM * 2));
-                h.r[F][CH][2 * X] = v.x;
-                h.r[F][CH][2 * X + 1] = v.y;
-            } else {
-                h.r[MR][CH] = *reinterpret_cast<const u32x4 *>(rb + (alongR ^ (half * 64 + CH * 32)) + MR * 4096);
-            }
+            h.r[F][CH] = *reinterpret_cast<const u32x4 *>(rb + (alongR ^ (half * 64 + CH * 32)) + F * 8192);
         }
     };
-    Acc acc[FC][FR];
-    // The products of a half, one matrix instruction after the other; dealt out between them the reads of the next
-    // half and, with REQUEST, the requests of step kq.
-    auto multiply = [&](auto request_too, const Half &h, Half &nx, const uint8_t *rb, const uint8_t *cb, int half, uint32_t rq,
-                        uint32_t cq) {
-        constexpr bool REQUEST = decltype(request_too)::value;
-        constexpr int kAll = 2 * FR * FC;
-        each<kAll>([&](auto n) {
-            constexpr int Nn = decltype(n)::value, CH = Nn / (FR * FC), J = Nn % (FR * FC) / FC, I = Nn % FC;
-            mfma_inplace(acc[I][J], h.c[I][CH], h.r[J][CH]);
-            constexpr int kFirst = Nn * kReads / kAll, kEnd = (Nn + 1) * kReads / kAll;
-            each<kEnd - kFirst>([&](auto m) { read(Const<kFirst + decltype(m)::value>{}, nx, rb, cb, half); });
-            if constexpr (REQUEST) {
-                constexpr int kFirstQ = Nn * (LR + LC) / kAll, kEndQ = (Nn + 1) * (LR + LC) / kAll;
-                each<kEndQ - kFirstQ>([&](auto m) { request(Const<kFirstQ + decltype(m)::value>{}, rq, cq); });
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        });
+    auto read_c = [&](auto f, auto ch, Half &h, const uint8_t *cb, int half) {
+        constexpr int F = decltype(f)::value, CH = decltype(ch)::value;
+        if constexpr (kTurnedC) {
+            const u32x2 lo = read_turned(cb + turnC[F] + (half * 32 + CH * 16) * (BN * 2));
+            const u32x2 hi = read_turned(cb + turnC[F] + (half * 32 + CH * 16 + 4) * (BN * 2));
+            h.c[F][CH] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            h.c[F][CH] = *reinterpret_cast<const u32x4 *>(cb + (alongC ^ (half * 64 + CH * 32)) + F * 4096);
+        }
     };
     // This wave's LDS reads are in its registers and all but its last `left` loads and stores are done; then all waves' are.
     auto meet = [&](auto left) {
@@ -375,15 +449,38 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    auto clear = [&] {
-#pragma unroll
-        for (int i = 0; i < FC; ++i)
-#pragma unroll
-            for (int n = 0; n < FR; ++n) {
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][n][v] = 0;
-                asm volatile("" : "+a"(acc[i][n]));
-            }
+    // The same where the results of `n` fragments of rows were stored since.
+    auto meet_behind = [&](int32_t n) {
+        constexpr int kPer = FC * 2 * (OUT32 ? 2 : 1);  // stores of a wave and fragment of rows
+        each<FR + 1>([&](auto f) {
+            constexpr int L = decltype(f)::value * kPer < 63 ? decltype(f)::value * kPer : 63;
+            if (n == decltype(f)::value) __builtin_amdgcn_s_waitcnt((L & 15) | (L >> 4) << 14 | 0x70);
+        });
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // LDS read n of a half, in the order in which the products need them.
+    constexpr int kReads = 2 * (FR + FC);
+    auto read = [&](auto n, Half &h, const uint8_t *rb, const uint8_t *cb, int half) {
+        constexpr int CH = decltype(n)::value / (FR + FC), M = decltype(n)::value % (FR + FC);
+        if constexpr (M == 0)
+            read_r(Const<0>{}, Const<CH>{}, h, rb, half);
+        else if constexpr (M <= FC)
+            read_c(Const<M - 1>{}, Const<CH>{}, h, cb, half);
+        else
+            read_r(Const<M - FC>{}, Const<CH>{}, h, rb, half);
+    };
+    // The products of a half, one matrix instruction after the other, NJ fragments of rows of them; between(n, of) is
+    // what goes behind product n of `of`, where the matrix instructions leave issue slots.
+    auto multiply = [&](auto nj, auto first, const Half &h, auto &&between) {
+        constexpr int NJ = decltype(nj)::value;
+        each<2 * NJ * FC>([&](auto n) {
+            constexpr int Nn = decltype(n)::value, CH = Nn / (NJ * FC), J = Nn % (NJ * FC) / FC, I = Nn % FC;
+            mfma_sums<I * FR + J, FC * FR, decltype(first)::value && CH == 0, INT8>(h.c[I][CH], h.r[J][CH]);
+            between(Const<Nn>{}, Const<2 * NJ * FC>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
 
     if constexpr (KIND == kDenseWeightsGrad) {
@@ -394,116 +491,124 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
     } else {
         fetch_entry(next);
     }
-    advance();
-    each<LR + LC>([&](auto t) { request(t, rto0, cto0); });
-    ++kq;
-    advance();
-    each<LR + LC>([&](auto t) { request(t, rto1, cto1); });
-    ++kq;
+    uint32_t at = 0;  // the places of step k: rows at `at`, columns behind them; of step k + 1 at at ^ kNext
+    constexpr uint32_t kNext = 2 * kPlace;
+    auto request_step = [&](uint32_t to) {
+        advance();
+        if constexpr (KIND == kDenseWeightsGrad) {
+            each<LR + LC>([&](auto t) { prepare(t); });
+            prepare_dead();
+        }
+        advance_lists();
+        each<LR + LC>([&](auto t) { request(t, to + (decltype(t)::value < LR ? 0 : kPlace)); });
+        ++kq;
+        meet(Const<0>{});
+    };
+    turn_to_next();
+    request_step(0);
+    request_step(kNext);
     DenseTile T = Q;  // the tile that is computed, step k of `steps`
     int32_t k = 0, steps = stepsQ;
-    clear();
-    meet(Const<0>{});
-    clear_tail(0, rbuf0, cbuf0);
+    clear_tail(0, 0);
+    auto rows_of = [&](const DenseTile &t) { return KIND == kDenseWeightsGrad ? min(P.N - t.r0, BM) : t.hi - t.lo; };
+    int32_t mine = ceil_div(rows_of(T), 64);  // fragments of rows of a wave
+    int32_t stored = 0;                       // of the tile before, whose results are on their way
     Half h0, h1;
-    each<kReads>([&](auto n) { read(n, h0, rbuf0, cbuf0, 0); });
+    each<kReads>([&](auto n) { read(n, h0, ring, ring + kPlace, 0); });
 
-    // Of the tile's rows, as its last step begins: the entries' weights (and scales), and which have no row.
-    float factor[FR];
-    float scale[FR];
-    int32_t rowOf[FR];
-    // Stores of results per wave and tile, whatever the tile holds.
-    constexpr int kStores = FC * FR * 2 * (OUT32 ? 2 : 1);
-    auto step = [&](const uint8_t *rb, const uint8_t *cb, uint8_t *ro, uint8_t *co, uint32_t rto, uint32_t cto) {
-        const bool last = k + 1 == steps;
-        if constexpr (KIND != kDenseWeightsGrad) {
-            if (last) {
-#pragma unroll
-                for (int n = 0; n < FR; ++n) {
-                    const int32_t ent = min(T.lo + wr + n * 32 + l31, T.hi - 1);
-                    rowOf[n] = P.entryRow ? P.entryRow[ent] : ent;
-                    factor[n] = P.entryWeight ? P.entryWeight[ent] : 1.0f;
-                }
+    auto step = [&](auto nj, auto first) {
+        constexpr bool FIRST = decltype(first)::value;
+        advance();
+        const uint8_t *const rb = ring + at, *const cb = rb + kPlace, *const ro = ring + (at ^ kNext), *const co = ro + kPlace;
+        constexpr int kLoads = LR + LC;
+        multiply(nj, first, h0, [&](auto n, auto of) {
+            constexpr int Nn = decltype(n)::value, kOf = decltype(of)::value;
+            constexpr int kFirst = Nn * kReads / kOf, kEnd = (Nn + 1) * kReads / kOf;
+            each<kEnd - kFirst>([&](auto m) { read(Const<kFirst + decltype(m)::value>{}, h1, rb, cb, 1); });
+            if constexpr (KIND == kDenseWeightsGrad) {
+                constexpr int kFirstP = Nn * kLoads / kOf, kEndP = (Nn + 1) * kLoads / kOf;
+                each<kEndP - kFirstP>([&](auto m) { prepare(Const<kFirstP + decltype(m)::value>{}); });
             }
-        }
-        multiply(Const<0>{}, h0, h1, rb, cb, 1, rto, cto);
-        if (k == 0)
-            meet(Const<kStores < 63 ? kStores : 63>{});  // step 1 was there before the results' stores
+        });
+        if constexpr (FIRST)
+            meet_behind(stored);  // step 1 was there before the results' stores
         else
             meet(Const<0>{});
-        if constexpr (KIND != kDenseWeightsGrad) {
-            if (last) {
-#pragma unroll
-                for (int n = 0; n < FR; ++n) {  // for the compiler: they have arrived here
-                    asm volatile("" : "+v"(rowOf[n]));
-                    asm volatile("" : "+v"(factor[n]));
-                }
-            }
-        }
-        if constexpr (INT8) {
-            if (last) {
-#pragma unroll
-                for (int n = 0; n < FR; ++n) {
-                    scale[n] = 0.0f;
-                    if ((uint32_t)rowOf[n] < (uint32_t)P.numRows) scale[n] = P.rowScales[rowOf[n]];
-                }
-            }
-        }
-        clear_tail(last ? 0 : k + 1, ro, co);
-        advance();
-        multiply(Const<1>{}, h1, h0, ro, co, 0, rto, cto);
-        ++kq;
-        ++k;
-        return last;
+        clear_tail(k + 1 == steps ? 0 : k + 1, at ^ kNext);
+        if constexpr (KIND == kDenseWeightsGrad) prepare_dead();
+        advance_lists();
+        multiply(nj, Const<0>{}, h1, [&](auto n, auto of) {
+            constexpr int Nn = decltype(n)::value, kOf = decltype(of)::value;
+            constexpr int kFirst = Nn * kReads / kOf, kEnd = (Nn + 1) * kReads / kOf;
+            each<kEnd - kFirst>([&](auto m) { read(Const<kFirst + decltype(m)::value>{}, h0, ro, co, 0); });
+            constexpr int kFirstQ = Nn * kLoads / kOf, kEndQ = (Nn + 1) * kLoads / kOf;
+            each<kEndQ - kFirstQ>([&](auto m) {
+                constexpr int M = kFirstQ + decltype(m)::value;
+                request(Const<M>{}, at + (M < LR ? 0 : kPlace));
+            });
+        });
+        ++kq, ++k;
+        at ^= kNext;
     };
     // Stores a tile's results and begins the next; false where there is none.
     auto finish = [&] {
         mfma_done();
         uint8_t *base;
-        int32_t rows;
-        if constexpr (KIND == kDenseWeightsGrad) {
+        if constexpr (KIND == kDenseWeightsGrad)
             base = P.out + ((int64_t)T.e * P.N + T.r0) * rowOut;
-            rows = min(P.N - T.r0, BM);
-        } else {
+        else
             base = P.out + (int64_t)T.lo * rowOut;
-            rows = T.hi - T.lo;
-        }
+        const int32_t bytes = rows_of(T) * rowOut;
         // a buffer that ends with the tile's last row; columns past the end are sent beyond it
-        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(base, 0, rows * rowOut, 0x00020000);
+        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(base, 0, bytes, 0x00020000);
         const __amdgpu_buffer_rsrc_t add = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t *>(KIND == kDenseWeightsGrad && P.base ? P.base + (base - P.out) : base), 0, rows * rowOut, 0x00020000);
+            const_cast<uint8_t *>(KIND == kDenseWeightsGrad && P.base ? P.base + (base - P.out) : base), 0, bytes, 0x00020000);
+        const int ln = fresh(), low = ln & 31, high = ln >> 5;
+        int32_t at0[FC][2], at1[FC][2];
+        float cs[FC][2][8];
 #pragma unroll
         for (int i = 0; i < FC; ++i) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const int32_t c = T.c0 + wc + i * 32 + p * 16 + far * 8;
-                float cs[8];
+                const int32_t c = T.c0 + wc + i * 32 + p * 16 + high * 8, outside = 0x7ffffff0;
+                const int32_t at = (wr + low) * rowOut + c * (OUT32 ? 4 : 2);
+                at0[i][p] = c < C ? at : outside;
+                at1[i][p] = c + 4 < C ? at + 16 : outside;
                 if constexpr (INT8) {
                     const float *s = P.weightScales + (int64_t)T.e * P.N;
                     const f32x4_dword lo = *reinterpret_cast<const f32x4_dword *>(s + min(c, P.N - 4));
                     const f32x4_dword hi = *reinterpret_cast<const f32x4_dword *>(s + min(c + 4, P.N - 4));
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) cs[v] = lo[v], cs[4 + v] = hi[v];
+                    for (int v = 0; v < 4; ++v) cs[i][p][v] = lo[v], cs[i][p][4 + v] = hi[v];
                 }
-#pragma unroll
-                for (int n = 0; n < FR; ++n) {
+            }
+        }
+        each<FR>([&](auto f) {
+            constexpr int F = decltype(f)::value;
+            if (F >= mine) return;
+            const uint32_t down = (uint32_t)(F * 64) * (uint32_t)rowOut;
+            RowInfo info{};
+            if constexpr (KIND != kDenseWeightsGrad) info = rowInfo[(turns & 1) ^ 1][wr + F * 64 + low];
+            each<FC * 2>([&](auto ip) {
+                constexpr int i = decltype(ip)::value / 2, p = decltype(ip)::value % 2;
+                {
                     float v[8];
-                    asm volatile("" : "+a"(acc[i][n]));  // not copied out before they are needed
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        v[x] = (float)acc[i][n][p * 8 + x];
-                        if constexpr (INT8) v[x] = v[x] * scale[n] * cs[x];
-                    }
-                    const int32_t outside = 0x7ffffff0, at = (wr + n * 32 + l31) * rowOut + c * (OUT32 ? 4 : 2);
-                    const int32_t at0 = c < C ? at : outside, at1 = c + 4 < C ? at + 16 : outside;
+                    each<8>([&](auto x) {
+                        constexpr int X = decltype(x)::value;
+                        const uint32_t sum = read_sum<i * FR + F, FC * FR, p * 8 + X>();
+                        if constexpr (INT8)
+                            v[X] = (float)(int32_t)sum * info.scale * cs[i][p][X];
+                        else
+                            v[X] = __uint_as_float(sum);
+                    });
+                    const int32_t to = (int32_t)(at0[i][p] + down), to1 = (int32_t)(at1[i][p] + down);
                     if constexpr (KIND != kDenseWeightsGrad) {
-                        const bool none = (uint32_t)rowOf[n] >= (uint32_t)P.numRows;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = none ? 0.0f : v[x] * factor[n];
+                        for (int x = 0; x < 8; ++x) v[x] = info.there ? v[x] * info.factor : 0.0f;
                     } else if (P.base) {
-                        const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(add, at0, 0, 0);
+                        const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(add, to, 0, 0);
                         if constexpr (OUT32) {
-                            const u32x4 a1 = __builtin_amdgcn_raw_buffer_load_b128(add, at1, 0, 0);
+                            const u32x4 a1 = __builtin_amdgcn_raw_buffer_load_b128(add, to1, 0, 0);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) v[x] += __uint_as_float(a[x]), v[4 + x] += __uint_as_float(a1[x]);
                         } else {
@@ -514,26 +619,46 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
                     }
                     if constexpr (OUT32) {
                         __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                                     __float_as_uint(v[3])}, out, at0, 0, 0);
+                                                                     __float_as_uint(v[3])}, out, to, 0, 0);
                         __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                                                                     __float_as_uint(v[7])}, out, at1, 0, 0);
+                                                                     __float_as_uint(v[7])}, out, to1, 0, 0);
                     } else {
                         __builtin_amdgcn_raw_buffer_store_b128(
-                            u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])}, out, at0, 0, 0);
+                            u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])}, out, to, 0, 0);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-        }
+            });
+        });
+        stored = mine;
         T = Q;
         k = 0;
         steps = stepsQ;
-        clear();
+        mine = ceil_div(rows_of(T), 64);
         return T.e >= 0;
     };
-    for (;;) {
-        if (step(rbuf0, cbuf0, rbuf1, cbuf1, rto0, cto0) && !finish()) break;
-        if (step(rbuf1, cbuf1, rbuf0, cbuf0, rto1, cto1) && !finish()) break;
+    // f(fragments of rows that a wave has in this tile), a constant
+    auto with_fragments = [&](auto &&f) {
+        if constexpr (FR == 4) {
+            if (mine > 3) return f(Const<4>{});
+            if (mine == 3) return f(Const<3>{});
+        }
+        if (mine > 1) return f(Const<2>{});
+        f(Const<1>{});
+    };
+    for (bool turned = false;;) {
+        if (!turned && k + 2 >= steps) {  // the last two steps request the next tile's first two
+            turn_to_next();
+            turned = true;
+        }
+        if (k == 0) with_fragments([&](auto nj) { step(nj, Const<1>{}); });
+        const int32_t until = turned ? steps : steps - 2;
+        with_fragments([&](auto nj) {
+            while (k < until) step(nj, Const<0>{});
+        });
+        if (k < steps) continue;
+        if (!finish()) break;
+        turned = false;
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // nothing of this wave is on its way into LDS when it ends
 }

@@ -83,16 +83,21 @@ __device__ __forceinline__ Groups count_tiles(const Params &P, int32_t NT) {
     return g;
 }
 
+// A tile among its expert's: group [lo, hi), row tile m of `tiles`, columns from n0.
+struct PlaceOf {
+    int32_t e, lo, hi, m, tiles, n0;
+};
+
 // Tile b among all experts' tiles (BM entries x BN columns), or e = -1 when
 // there are fewer.  Each XCD (block b % 8) takes a contiguous stretch of the
 // tiles, so the tiles that run on it together share operands in its L2;
 // within an expert, bands of four row tiles (up to seven where four would
 // leave a rest) go through the columns together.
 template <int BM, int BN, class Params>
-__device__ __forceinline__ TileAt find_tile(const Params &P, Groups &g, int32_t NT, int32_t b) {
+__device__ __forceinline__ PlaceOf find_place(const Params &P, Groups &g, int32_t NT, int32_t b) {
     const int64_t per = (g.total + 7) / 8;
     const int64_t at = (b & 7) * per + (b >> 3);
-    TileAt t{-1, 0, 0, 0};
+    PlaceOf t{-1, 0, 0, 0, 0, 0};
     if ((b >> 3) >= per || at >= g.total) return t;
     int64_t before = 0;
     int32_t least = P.maxEntries;
@@ -107,12 +112,18 @@ __device__ __forceinline__ TileAt find_tile(const Params &P, Groups &g, int32_t 
             const int32_t size = ceil_div(tiles, max(tiles >> 2, 1));  // row tiles of a band
             const int32_t band = r0 / (size * NT), rows = min(size, tiles - band * size), r = r0 - band * size * NT;
             const int32_t n = r / rows, m = band * size + r - n * rows;
-            t = TileAt{uniform(e0 + f), uniform(lo + m * BM), uniform(min(hi, lo + m * BM + BM)), uniform(n * BN)};
-            return t;
+            return PlaceOf{e0 + f, lo, hi, m, tiles, n * BN};
         }
         before += uniform(__shfl(g.incl, 63));
     }
     return t;
+}
+
+template <int BM, int BN, class Params>
+__device__ __forceinline__ TileAt find_tile(const Params &P, Groups &g, int32_t NT, int32_t b) {
+    const PlaceOf t = find_place<BM, BN>(P, g, NT, b);
+    if (t.e < 0) return TileAt{-1, 0, 0, 0};
+    return TileAt{uniform(t.e), uniform(t.lo + t.m * BM), uniform(min(t.hi, t.lo + t.m * BM + BM)), uniform(t.n0)};
 }
 
 }  // namespace
