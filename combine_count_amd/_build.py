@@ -8,13 +8,15 @@ from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libepdc.so")
 SOURCES = ["epdc_api.cpp", "epdc_api_ops.cpp", "epdc_api_experts.cpp", "dispatch.hip", "combine.hip", "combine_push.hip",
-           "route.hip", "mx.hip", "group.hip", "product.hip", "product_dense.hip", "gate.hip", "int8.hip"]
+           "route.hip", "mx.hip", "group.hip", "product.hip", "dense_linear.hip", "dense_linear_int.hip",
+           "dense_rows_grad.hip", "dense_weights_grad.hip", "gate.hip", "int8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [
@@ -28,23 +30,24 @@ DEVICE = ["-x", "hip", "--offload-arch=gfx950", "-Xclang", "-target-feature", "-
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
-    for src in SOURCES:
-        path = os.path.join(CSRC, src)
+    def compile_one(src):
         obj = os.path.join(BUILD, src + ".o")
-        lang = DEVICE if src.endswith(".hip") else []
-        cmd = [HIPCC, *lang, *COMMON, "-c", path, "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        # hipcc's host pass does not know the device feature flag: drop that note
-        noise = "is not a recognized feature for this target"
-        msg = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l)
-        if msg.strip() and (verbose or r.returncode):
-            print(msg, flush=True)
-        if r.returncode:
-            raise subprocess.CalledProcessError(r.returncode, cmd)
-        objs.append(obj)
+        cmd = [HIPCC, *(DEVICE if src.endswith(".hip") else []), *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+        return obj, cmd, subprocess.run(cmd, capture_output=True, text=True)
+
+    objs = []
+    with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:  # the products' kernels take half a minute a file
+        for obj, cmd, r in pool.map(compile_one, sorted(SOURCES, key=lambda s: not s.startswith("dense"))):
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            # hipcc's host pass does not know the device feature flag: drop that note
+            noise = "is not a recognized feature for this target"
+            msg = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l)
+            if msg.strip() and (verbose or r.returncode):
+                print(msg, flush=True)
+            if r.returncode:
+                raise subprocess.CalledProcessError(r.returncode, cmd)
+            objs.append(obj)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -107,7 +107,8 @@ int epdc_expert_linear(int32_t numExperts, int32_t numCols, int32_t hiddenDim, i
         rc = product_params(numExperts, numCols, hiddenDim, maxEntries, numRows, rows, offsets, entryRow, entryWeight, weights,
                             out, P);
         if (rc != EPDC_OK) return rc;
-        return hip_status(epdc::launch_dense(P, epdc::kDenseProduct, false, outDtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
+        return hip_status(epdc::launch_dense_linear(P, epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries), outDtype == EPDC_FP32,
+                                             static_cast<hipStream_t>(stream)),
                           "bf16 product launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_linear");
@@ -125,7 +126,8 @@ int epdc_expert_rows_grad(int32_t numExperts, int32_t numCols, int32_t hiddenDim
         rc = product_params(numExperts, numCols, hiddenDim, maxEntries, numRows, dOut, offsets, entryRow, entryWeight, weights,
                             dRows, P);
         if (rc != EPDC_OK) return rc;
-        return hip_status(epdc::launch_dense(P, epdc::kDenseRowsGrad, false, dtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
+        return hip_status(epdc::launch_dense_rows_grad(P, epdc::plan_dense(epdc::kDenseRowsGrad, P.E, P.N, P.H, P.maxEntries), dtype == EPDC_FP32,
+                                             static_cast<hipStream_t>(stream)),
                           "rows' gradient launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_rows_grad");
@@ -163,7 +165,8 @@ int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hidden
         P.outRow = outRow;
         P.base = static_cast<const uint8_t *>(base);
         P.out = static_cast<uint8_t *>(dWeights);
-        return hip_status(epdc::launch_dense(P, epdc::kDenseWeightsGrad, false, dtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
+        return hip_status(epdc::launch_dense_weights_grad(P, epdc::plan_dense(epdc::kDenseWeightsGrad, P.E, P.N, P.H, P.maxEntries), dtype == EPDC_FP32,
+                                             static_cast<hipStream_t>(stream)),
                           "weights' gradient launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_weights_grad");
@@ -187,7 +190,8 @@ int epdc_expert_linear_int(int32_t numExperts, int32_t numCols, int32_t hiddenDi
             return fail(EPDC_ERR_ALIGN, "rowScales and weightScales must be 4-byte aligned");
         P.rowScales = rowScales;
         P.weightScales = weightScales;
-        return hip_status(epdc::launch_dense(P, epdc::kDenseProduct, true, outDtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
+        return hip_status(epdc::launch_dense_linear_int(P, epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries), outDtype == EPDC_FP32,
+                                             static_cast<hipStream_t>(stream)),
                           "int8 product launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_linear_int");

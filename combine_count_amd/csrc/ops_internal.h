@@ -1,7 +1,7 @@
 // Kernel parameters and launchers of the operators next to dispatch and
 // combine: routing (route.hip), fp4x2 quantisation (mx.hip), grouping by
 // expert (group.hip), the experts' product (product.hip), and the experts in
-// bf16 and int8 (product_dense.hip, gate.hip, int8.hip).  Not part of the C ABI.
+// bf16 and int8 (product_dense.h, gate.hip, int8.hip).  Not part of the C ABI.
 #pragma once
 
 #include "epdc_internal.h"
@@ -241,7 +241,10 @@ hipError_t launch_mx_dequantize(const MxParams &p, bool fp32, hipStream_t stream
 int64_t group_scratch_words(int32_t W, int32_t M, int32_t K, int32_t Epr);
 hipError_t launch_group(const GroupParams &p, hipStream_t stream);
 hipError_t launch_product(const ProductParams &p, bool out32, hipStream_t stream);
-hipError_t launch_dense(const DenseParams &p, DenseKind kind, bool int8, bool out32, hipStream_t stream);
+hipError_t launch_dense_linear(const DenseParams &p, DenseForm form, bool out32, hipStream_t stream);
+hipError_t launch_dense_linear_int(const DenseParams &p, DenseForm form, bool out32, hipStream_t stream);
+hipError_t launch_dense_rows_grad(const DenseParams &p, DenseForm form, bool out32, hipStream_t stream);
+hipError_t launch_dense_weights_grad(const DenseParams &p, DenseForm form, bool out32, hipStream_t stream);
 hipError_t launch_gate(const GateParams &p, bool fp32, bool out32, hipStream_t stream);
 hipError_t launch_gate_grad(const GateParams &p, bool fp32, bool out32, hipStream_t stream);
 hipError_t launch_gate_int(const GateParams &p, bool fp32, hipStream_t stream);

@@ -6,6 +6,8 @@
 //
 // Tiles of 256 x 256 or 128 x 128 of the output, through LDS, with
 // v_mfma_f32_32x32x16_bf16 (v_mfma_i32_32x32x32_i8); plan_dense chooses.
+#pragma once
+
 #include "tiles.h"
 
 namespace epdc {
@@ -15,45 +17,44 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_dword __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at 4-byte alignment
 
 // The sums of 32 x 32 products stay in accumulation registers of their own,
-// named here (fragment f: a16f .. a16f + 15) and marked as overwritten by every
-// statement that touches them, so that the compiler keeps nothing there: its own
-// allocation of 256 of them moved them about or spilled where the kernel has
-// several bodies.  It does not see the matrix instruction: its operands must not
+// named here (fragment f: a16f .. a16f + 15): the compiler's own allocation of
+// 256 of them moved them about or spilled where the kernel has several bodies.
+// It sees them as overwritten in every half of a step (hold_sums), so that it
+// keeps nothing there; that it does not use them in between either is checked on
+// the built code.  It does not see the matrix instruction: its operands must not
 // come from a vector instruction just before it, and its sums are read behind
 // mfma_done().
-#define EPDC_A8(n) "a" #n "0", "a" #n "1", "a" #n "2", "a" #n "3", "a" #n "4", "a" #n "5", "a" #n "6", "a" #n "7", "a" #n "8", "a" #n "9"
+#define EPDC_A10(n) "a" #n "0", "a" #n "1", "a" #n "2", "a" #n "3", "a" #n "4", "a" #n "5", "a" #n "6", "a" #n "7", "a" #n "8", "a" #n "9"
 #define EPDC_SUMS64 \
-    "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", EPDC_A8(1), EPDC_A8(2), EPDC_A8(3), EPDC_A8(4), EPDC_A8(5), "a60", "a61", "a62", "a63"
+    "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", EPDC_A10(1), EPDC_A10(2), EPDC_A10(3), EPDC_A10(4), EPDC_A10(5), "a60", "a61", "a62", "a63"
 #define EPDC_SUMS256 \
-    EPDC_SUMS64, "a64", "a65", "a66", "a67", "a68", "a69", EPDC_A8(7), EPDC_A8(8), EPDC_A8(9), EPDC_A8(10), EPDC_A8(11), EPDC_A8(12), EPDC_A8(13), \
-        EPDC_A8(14), EPDC_A8(15), EPDC_A8(16), EPDC_A8(17), EPDC_A8(18), EPDC_A8(19), EPDC_A8(20), EPDC_A8(21), EPDC_A8(22), EPDC_A8(23), EPDC_A8(24), \
+    EPDC_SUMS64, "a64", "a65", "a66", "a67", "a68", "a69", EPDC_A10(7), EPDC_A10(8), EPDC_A10(9), EPDC_A10(10), EPDC_A10(11), EPDC_A10(12), EPDC_A10(13), \
+        EPDC_A10(14), EPDC_A10(15), EPDC_A10(16), EPDC_A10(17), EPDC_A10(18), EPDC_A10(19), EPDC_A10(20), EPDC_A10(21), EPDC_A10(22), EPDC_A10(23), EPDC_A10(24), \
         "a250", "a251", "a252", "a253", "a254", "a255"
-#define EPDC_MFMA(NAME, SUMS)                                                                                                     \
-    if constexpr (FIRST)                                                                                                          \
-        asm volatile(NAME " a[%2:%3], %0, %1, 0" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15) : SUMS);                       \
-    else                                                                                                                          \
-        asm volatile(NAME " a[%2:%3], %0, %1, a[%2:%3]" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15) : SUMS);
-// Fragment F of a wave's ALL (4 or 16): += a . b, or with FIRST = a . b.
-template <int F, int ALL, bool FIRST, bool INT8>
+template <int ALL>
+__device__ __forceinline__ void hold_sums() {
+    if constexpr (ALL == 16)
+        asm volatile("" : : : EPDC_SUMS256);
+    else
+        asm volatile("" : : : EPDC_SUMS64);
+}
+// Fragment F: += a . b, or with FIRST = a . b.
+template <int F, bool FIRST, bool INT8>
 __device__ __forceinline__ void mfma_sums(u32x4 a, u32x4 b) {
-    if constexpr (INT8 && ALL == 16) {
-        EPDC_MFMA("v_mfma_i32_32x32x32_i8", EPDC_SUMS256)
-    } else if constexpr (INT8) {
-        EPDC_MFMA("v_mfma_i32_32x32x32_i8", EPDC_SUMS64)
-    } else if constexpr (ALL == 16) {
-        EPDC_MFMA("v_mfma_f32_32x32x16_bf16", EPDC_SUMS256)
-    } else {
-        EPDC_MFMA("v_mfma_f32_32x32x16_bf16", EPDC_SUMS64)
-    }
+    if constexpr (INT8 && FIRST)
+        asm volatile("v_mfma_i32_32x32x32_i8 a[%2:%3], %0, %1, 0" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15));
+    else if constexpr (INT8)
+        asm volatile("v_mfma_i32_32x32x32_i8 a[%2:%3], %0, %1, a[%2:%3]" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15));
+    else if constexpr (FIRST)
+        asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, 0" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15));
+    else
+        asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]" : : "v"(a), "v"(b), "n"(F * 16), "n"(F * 16 + 15));
 }
 // Sum V of fragment F, as it lies in the register.
-template <int F, int ALL, int V>
+template <int F, int V>
 __device__ __forceinline__ uint32_t read_sum() {
     uint32_t x;
-    if constexpr (ALL == 16)
-        asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(F * 16 + V) : EPDC_SUMS256);
-    else
-        asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(F * 16 + V) : EPDC_SUMS64);
+    asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(F * 16 + V));
     return x;
 }
 
@@ -475,9 +476,10 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
     // what goes behind product n of `of`, where the matrix instructions leave issue slots.
     auto multiply = [&](auto nj, auto first, const Half &h, auto &&between) {
         constexpr int NJ = decltype(nj)::value;
+        hold_sums<FC * FR>();
         each<2 * NJ * FC>([&](auto n) {
             constexpr int Nn = decltype(n)::value, CH = Nn / (NJ * FC), J = Nn % (NJ * FC) / FC, I = Nn % FC;
-            mfma_sums<I * FR + J, FC * FR, decltype(first)::value && CH == 0, INT8>(h.c[I][CH], h.r[J][CH]);
+            mfma_sums<I * FR + J, decltype(first)::value && CH == 0, INT8>(h.c[I][CH], h.r[J][CH]);
             between(Const<Nn>{}, Const<2 * NJ * FC>{});
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -591,11 +593,12 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
             if constexpr (KIND != kDenseWeightsGrad) info = rowInfo[(turns & 1) ^ 1][wr + F * 64 + low];
             each<FC * 2>([&](auto ip) {
                 constexpr int i = decltype(ip)::value / 2, p = decltype(ip)::value % 2;
+                hold_sums<FC * FR>();
                 {
                     float v[8];
                     each<8>([&](auto x) {
                         constexpr int X = decltype(x)::value;
-                        const uint32_t sum = read_sum<i * FR + F, FC * FR, p * 8 + X>();
+                        const uint32_t sum = read_sum<i * FR + F, p * 8 + X>();
                         if constexpr (INT8)
                             v[X] = (float)(int32_t)sum * info.scale * cs[i][p][X];
                         else
@@ -630,6 +633,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
                 }
             });
         });
+        hold_sums<FC * FR>();
         stored = mine;
         T = Q;
         k = 0;
@@ -686,19 +690,4 @@ hipError_t launch_tiles(const DenseParams &P, bool out32, hipStream_t stream) {
 }
 
 }  // namespace
-
-hipError_t launch_dense(const DenseParams &P, DenseKind kind, bool int8, bool out32, hipStream_t stream) {
-    const bool large = plan_dense(kind, P.E, P.N, P.H, P.maxEntries) == kDenseTiles256;
-    switch (kind) {
-    case kDenseProduct:
-        if (int8) return large ? launch_tiles<kDenseProduct, true, 256, 256>(P, out32, stream) : launch_tiles<kDenseProduct, true, 128, 128>(P, out32, stream);
-        return large ? launch_tiles<kDenseProduct, false, 256, 256>(P, out32, stream) : launch_tiles<kDenseProduct, false, 128, 128>(P, out32, stream);
-    case kDenseRowsGrad:
-        return large ? launch_tiles<kDenseRowsGrad, false, 256, 256>(P, out32, stream) : launch_tiles<kDenseRowsGrad, false, 128, 128>(P, out32, stream);
-    case kDenseWeightsGrad:
-        return large ? launch_tiles<kDenseWeightsGrad, false, 256, 256>(P, out32, stream) : launch_tiles<kDenseWeightsGrad, false, 128, 128>(P, out32, stream);
-    }
-    return hipErrorInvalidValue;
-}
-
 }  // namespace epdc

