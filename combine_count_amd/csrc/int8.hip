@@ -11,7 +11,7 @@
 // The activation's codes are those of its values in 64 bits.  A 32-bit value a
 // of it is within 2^-20 |a|: where a / scale is that near the border between
 // two codes, or a that near the row's maximum, the value is taken again in 64
-// bits (one element in 2000, and about one a row).
+// bits (one element in 1000, and about one a row).
 #include "expert_elems.h"
 
 namespace epdc {
@@ -85,12 +85,22 @@ __global__ __launch_bounds__(256) void int_quantize_kernel(Int8Params P, DivMagi
     for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) codes(to_eight<FP32>(load_raw8<FP32>(x, unit)), unit);
 }
 
-// The activation's value, in 64 bits, rounded to fp32.
+// The activation's value, in 64 bits, rounded to fp32.  Out of line: few lanes get here.
 __device__ __noinline__ float gate_exactly(float g, float u, float w) {
     const double s = 1.0 / (1.0 + exp(-(double)g));
     return (float)((double)g * s * (double)u * (double)w);
 }
 
+// A value's error in 32 bits: an exponential, a quotient and four products,
+// below 12 half steps, so 2^-20 of it with room -- unless a factor leaves fp32's
+// normal range on the way.  With the bounds below what is lost there is under
+// 88 * 2^-126 * 2^30 * 2^15, 2^-27 of a code of a row whose maximum is above 2^-40.
+constexpr float kClose = 0x1p-20f;
+__device__ __forceinline__ bool plain_factors(float u, float w) { return fabsf(u) < 0x1p30f && w < 0x1p15f && w > 0x1p-15f; }
+
+// A lane's first eight values stay in registers (the others are computed again)
+// between three passes: the maximum in 32 bits; the maximum in 64 bits, of the
+// values close to it; the codes.
 template <bool FP32, int TEAM>
 __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
     __shared__ uint32_t part[4];
@@ -100,23 +110,66 @@ __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
     const int32_t lane = threadIdx.x % TEAM, units = P.F / 8;
     const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4);
     const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
+    struct Unit {
+        Raw8<FP32> g, u;
+        Eight a;
+    };
+    auto load = [&](int32_t unit) {
+        Unit x{load_raw8<FP32>(h, unit), load_raw8<FP32>(h, units + unit), {}};
+        const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // 1 / (1 + t) to a step
+            const float t = expf(-fabsf(g.v[j])), large = __builtin_amdgcn_rcpf(1.0f + t);
+            x.a.v[j] = g.v[j] * (g.v[j] >= 0.0f ? large : t * large) * u.v[j] * w;
+        }
+        return x;
+    };
+    auto each_value = [&](const Unit &x, auto &&f) {  // f(place, value in 32 bits, g, u)
+        const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(j, x.a.v[j], g.v[j], u.v[j]);
+    };
+    Unit kept{};
+    if (lane < units) kept = load(lane);
+    auto each_unit = [&](auto &&f) {
+        if (lane < units) f(kept, lane);
+        for (int32_t unit = lane + TEAM; unit < units; unit += TEAM) f(load(unit), unit);
+    };
     uint32_t most = 0;
-    for (int32_t unit = lane; unit < units; unit += TEAM) {
-        const Eight g = to_eight<FP32>(load_raw8<FP32>(h, unit)), u = to_eight<FP32>(load_raw8<FP32>(h, units + unit));
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) most = max(most, magnitude(gate_exactly(g.v[j], u.v[j], w)));
-    }
+    bool odd = false;  // factors beyond the bounds
+    each_unit([&](const Unit &x, int32_t) {
+        each_value(x, [&](int, float a, float, float u) {
+            most = max(most, magnitude(a));
+            odd |= !plain_factors(u, P.entryWeight ? fabsf(w) : 1.0f);
+        });
+    });
+    most = team_max<TEAM>(most, part);
+    // A row of odd factors, or of values beyond the middle of fp32's range: every value in 64 bits.
+    const bool all = team_max<TEAM>(odd, part) != 0 || !(__uint_as_float(most) > 0x1p-40f && __uint_as_float(most) < 0x1p100f);
+    const float near = __uint_as_float(most) * (1.0f - 2 * kClose);
+    most = 0;
+    each_unit([&](const Unit &x, int32_t) {
+        each_value(x, [&](int, float a, float g, float u) {
+            if (all || fabsf(a) >= near) most = max(most, magnitude(gate_exactly(g, u, w)));
+        });
+    });
     most = team_max<TEAM>(most, part);
     const float scale = scale_of(most);
     if (lane == 0) P.perEntry[row] = scale;
     const bool none = !(scale > 0.0f);
-    for (int32_t unit = lane; unit < units; unit += TEAM) {
-        const Eight g = to_eight<FP32>(load_raw8<FP32>(h, unit)), u = to_eight<FP32>(load_raw8<FP32>(h, units + unit));
+    const float over = 1.0f / scale;
+    each_unit([&](const Unit &x, int32_t unit) {
         int32_t c[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = none ? 0 : code_of(gate_exactly(g.v[j], u.v[j], w), scale);
+        each_value(x, [&](int j, float a, float g, float u) {
+            // Far enough from the border between two codes the quotient's last bits do not count: at 127 a value's
+            // error is 2^-13 of a code, this product's another 2^-16.
+            const float q = a * over, r = rintf(q);
+            c[j] = (int32_t)fminf(fmaxf(r, -127.0f), 127.0f);
+            if (all || fabsf(fabsf(q - r) - 0.5f) < 0x1p-11f) c[j] = none ? 0 : code_of(gate_exactly(g, u, w), scale);
+        });
         store_codes(P.out + (int64_t)row * P.F, unit, c);
-    }
+    });
 }
 
 }  // namespace
