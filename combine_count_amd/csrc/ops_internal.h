@@ -170,16 +170,38 @@ struct DenseParams {
 // out = rows . weights^T; dRows = dOut . weights; dWeights = dOut^T . rows
 enum DenseKind { kDenseProduct, kDenseRowsGrad, kDenseWeightsGrad };
 
-// Their kernels: tiles of 128 x 128 or 256 x 256 of the output.
-enum DenseForm { kDenseTiles128, kDenseTiles256 };
+// Their kernels: weights streamed into registers for tiles of 16 or 64 entries
+// (the product), tiles of 128 x 128 or 256 x 256 of the output through LDS.
+enum DenseForm { kDenseStream16, kDenseStream64, kDenseTiles128, kDenseTiles256 };
 
+// Which kernel, from the entries that can occur (the groups' sizes are known on
+// the device only).  Times in us, bf16, 7168 -> 4096 unless stated:
+//   * weights streamed where 128x128 tiles would leave CUs idle and experts have
+//     few entries: one expert, 16 / 64 entries 28 / 49 against 105 with tiles; 8
+//     experts, 64 entries 97 against 118; but 32 experts, 64 entries 352 against
+//     307.  Tiles of 64 entries beyond 16 an expert: 2 experts, 64 entries 39
+//     against 50 with 16; 4 experts, 128 entries 73 against 97 (128x128: 109); but
+//     8 experts, 256 entries 142 against 120 with 128x128; one expert, 256 / 512
+//     entries 87 / 173 against 105;
+//   * 256x256 tiles where the mean group fills a good part of one and there is
+//     one for every CU: 8 experts, 4096 / 2048 entries 219 / 202 against 284 /
+//     159; 32 experts, 4096 entries 419 against 385; 32 experts, 2048 -> 7168,
+//     8192 entries 293 against 324; one expert, 8192 / 2048 entries 357 / 138
+//     against 427 / 113;
+//   * the weights' gradient likewise (its tiles are all there, whatever the
+//     groups): 16 experts, 1024 x 1024, 256 tiles: 16384 / 333 entries 39 / 15.5
+//     against 47 / 16.3; 32 experts, 7168 -> 4096, 4096 entries, fp32 759 against 1057.
 inline DenseForm plan_dense(DenseKind kind, int32_t E, int32_t N, int32_t H, int32_t maxEntries) {
     const int32_t columns = kind == kDenseProduct ? N : H;
     if (kind == kDenseWeightsGrad)
         return (int64_t)E * ceil_div(N, 256) * ceil_div(H, 256) >= 256 ? kDenseTiles256 : kDenseTiles128;
+    const int32_t mean = ceil_div(maxEntries, E);
     const int64_t groups = E < maxEntries ? E : maxEntries;
+    const int64_t tiles128 = (maxEntries / 128 + groups) * ceil_div(columns, 128);
     const int64_t tiles256 = (maxEntries / 256 + groups / 2) * ceil_div(columns, 256);
-    return ceil_div(maxEntries, E) >= 96 && tiles256 >= 512 ? kDenseTiles256 : kDenseTiles128;
+    if (kind == kDenseProduct && mean <= 16 && tiles128 <= 288) return kDenseStream16;
+    if (kind == kDenseProduct && ((mean <= 128 && tiles128 <= 192) || (mean <= 256 && tiles128 <= 96))) return kDenseStream64;
+    return mean >= 192 && tiles256 >= 256 ? kDenseTiles256 : kDenseTiles128;
 }
 
 struct GateParams {

@@ -610,6 +610,21 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
             const uint32_t down = (uint32_t)(F * 64) * (uint32_t)rowOut;
             RowInfo info{};
             if constexpr (KIND != kDenseWeightsGrad) info = rowInfo[(turns & 1) ^ 1][wr + F * 64 + low];
+            // What the gradient is added to, of all the fragment's columns at once: so many loads are under way together.
+            constexpr int kAdd = KIND == kDenseWeightsGrad ? FC : 1, kAddRuns = OUT32 ? 2 : 1;
+            u32x4 before[kAdd][2][kAddRuns];
+            if (KIND == kDenseWeightsGrad && P.base) {
+#pragma unroll
+                for (int i = 0; i < kAdd; ++i)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int32_t c = T.c0 + wc + i * 32 + p * 16 + high * 8;
+                        const int32_t from = (int32_t)((wr + low) * rowOut + c * (OUT32 ? 4 : 2) + down);
+#pragma unroll
+                        for (int q = 0; q < kAddRuns; ++q)
+                            before[i][p][q] = __builtin_amdgcn_raw_buffer_load_b128(add, c < C ? from + q * 16 : outside, 0, 0);
+                    }
+            }
             each<FC>([&](auto ii) {
                 constexpr int i = decltype(ii)::value;
                 // v[p]: columns 16 p + 8 high .. + 7 of row `low`
@@ -629,17 +644,14 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
                 } else if (P.base) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const int32_t c = T.c0 + wc + i * 32 + p * 16 + high * 8;
-                        const int32_t from = (int32_t)((wr + low) * rowOut + c * (OUT32 ? 4 : 2) + down);
-                        const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(add, c < C ? from : outside, 0, 0);
+                        const u32x4(&a)[kAddRuns] = before[i % kAdd][p];
                         if constexpr (OUT32) {
-                            const u32x4 a1 = __builtin_amdgcn_raw_buffer_load_b128(add, c < C ? from + 16 : outside, 0, 0);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) v[p][x] += __uint_as_float(a[x]), v[p][4 + x] += __uint_as_float(a1[x]);
+                            for (int x = 0; x < 8; ++x) v[p][x] += __uint_as_float(a[x / 4 % kAddRuns][x % 4]);
                         } else {
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                v[p][2 * x] += __uint_as_float(a[x] << 16), v[p][2 * x + 1] += __uint_as_float(a[x] & 0xffff0000u);
+                                v[p][2 * x] += __uint_as_float(a[0][x] << 16), v[p][2 * x + 1] += __uint_as_float(a[0][x] & 0xffff0000u);
                         }
                     }
                 }

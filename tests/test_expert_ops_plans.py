@@ -10,7 +10,7 @@ import pytest
 from combine_count_amd import _build as B
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-FORMS = ("tiles128", "tiles256")
+FORMS = ("stream16", "stream64", "tiles128", "tiles256")
 PRODUCT, ROWS, WEIGHTS = 0, 1, 2
 
 
@@ -32,7 +32,23 @@ def plan(tmp_path_factory):
 
 # (kind, experts, columns, hidden, maxEntries): form
 EXPECT = {
+    # few entries, and tiles of 128 would leave CUs idle
+    (PRODUCT, 1, 4096, 7168, 1): "stream16",
+    (PRODUCT, 1, 4096, 7168, 16): "stream16",
+    (PRODUCT, 1, 4096, 7168, 64): "stream64",
+    (PRODUCT, 2, 4096, 7168, 64): "stream64",
+    (PRODUCT, 4, 4096, 7168, 128): "stream64",
+    (PRODUCT, 8, 4096, 7168, 64): "stream16",
+    (PRODUCT, 8, 4096, 7168, 256): "tiles128",
+    (PRODUCT, 1, 4096, 7168, 256): "stream64",
+    (PRODUCT, 1, 4096, 7168, 512): "tiles128",
     (PRODUCT, 32, 4096, 7168, 64): "tiles128",
+    # the mean group fills a good part of a 256-row tile, and there is one for every CU
+    (PRODUCT, 8, 4096, 7168, 2048): "tiles128",
+    (PRODUCT, 8, 4096, 7168, 4096): "tiles256",
+    (PRODUCT, 32, 4096, 7168, 4096): "tiles128",
+    (PRODUCT, 32, 7168, 2048, 8192): "tiles256",
+    (PRODUCT, 1, 4096, 7168, 8192): "tiles256",
     (PRODUCT, 32, 7168, 2048, 2047): "tiles128",
     (PRODUCT, 32, 4096, 7168, 32768): "tiles256",
     (ROWS, 8, 520, 1000, 777): "tiles128",
@@ -56,5 +72,6 @@ def test_the_gpu_tests_reach_every_form(plan):
     for kind in (PRODUCT, ROWS, WEIGHTS):
         small = [(kind, len(sizes), N, H, sum(sizes) + first + behind) for sizes, first, behind in T.GROUPS.values()
                  for N, H in T.SHAPES]
-        # ninety experts' gradients of larger weights are tiles enough for the other form
-        assert set(plan(small).values()) == ({"tiles128", "tiles256"} if kind == WEIGHTS else {"tiles128"})
+        # ninety experts of larger weights are tiles enough for the next form
+        want = {PRODUCT: {"stream16", "stream64", "tiles128"}, ROWS: {"tiles128"}, WEIGHTS: {"tiles128", "tiles256"}}
+        assert set(plan(small).values()) == want[kind]

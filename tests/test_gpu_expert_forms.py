@@ -14,6 +14,7 @@ BF16, FP32 = torch.bfloat16, torch.float32
 KIND = {BF16: epdc.EPDC_BF16, FP32: epdc.EPDC_FP32}
 SIZES = [700, 0, 1, 256, 515]  # entries of the experts
 LONG = 21896                   # columns (of the product; of the rows' gradient): 86 tiles of 256, the last a part
+SHORT = 1160                   # columns of the product for tiles of 128: 10 of them, the last a part
 # elements of the summed index: 1 to 5 steps of 128 bytes, whole and with endings
 BF16_TERMS = [8, 56, 64, 72, 120, 128, 136, 192, 200, 256, 264, 320]
 INT8_TERMS = [16, 112, 128, 144, 256, 272, 384, 400, 512, 528]
@@ -25,7 +26,7 @@ GRAD_SHAPE = (1288, 1544)      # 6 x 7 tiles of 256 an expert
 def product_shapes():
     """(form, kind, experts, columns, hidden, maxEntries), kinds 0: product, 1: rows' gradient, 2: weights' gradient"""
     n = sum(SIZES)
-    out = [("tiles256", 0, len(SIZES), LONG, t, n) for t in BF16_TERMS + INT8_TERMS]
+    out = [(form, 0, len(SIZES), cols, t, n) for form, cols in (("tiles256", LONG), ("tiles128", SHORT)) for t in BF16_TERMS + INT8_TERMS]
     out += [("tiles256", 1, len(SIZES), t, LONG, n) for t in BF16_TERMS]
     return out + [("tiles256", 2, len(GRAD_SIZES), *GRAD_SHAPE, sum(GRAD_SIZES))]
 
@@ -56,34 +57,36 @@ def _rows(g, n, R):
     return row
 
 
+@pytest.mark.parametrize("cols", [LONG, SHORT], ids=["tiles256", "tiles128"])
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("terms", BF16_TERMS)
-def test_product_tiles256(terms, dtype):
+def test_product_tiles(terms, dtype, cols):
     g = _gen(terms)
     o, off = _offsets(SIZES)
     n, R = o[-1], 901
     x = torch.randn(R, terms, device="cuda", generator=g).to(BF16)
-    b = torch.randn(len(SIZES), LONG, terms, device="cuda", generator=g).to(BF16)
+    b = torch.randn(len(SIZES), cols, terms, device="cuda", generator=g).to(BF16)
     row, w = _rows(g, n, R), torch.randn(n, device="cuda", generator=g)
-    out = torch.full((n + 2, LONG), 5.0, device="cuda", dtype=dtype)
-    epdc.epdc_expert_linear(len(SIZES), LONG, terms, n, R, x, off, row, w, b, out, KIND[dtype])
+    out = torch.full((n + 2, cols), 5.0, device="cuda", dtype=dtype)
+    epdc.epdc_expert_linear(len(SIZES), cols, terms, n, R, x, off, row, w, b, out, KIND[dtype])
     ref, size = O.product(x, o, row, w, b, n, out)
     _check(out, ref, O.product_bound(ref, size, terms, dtype), terms)
     assert (out[n:] == 5).all()
 
 
+@pytest.mark.parametrize("cols", [LONG, SHORT], ids=["tiles256", "tiles128"])
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("terms", INT8_TERMS)
-def test_product_int8_tiles256(terms, dtype):
+def test_product_int8_tiles(terms, dtype, cols):
     g = _gen(terms)
     o, off = _offsets(SIZES)
     n, R = o[-1], 901
     x = torch.randint(-127, 128, (R, terms), device="cuda", generator=g, dtype=torch.int16).to(torch.int8)
-    b = torch.randint(-127, 128, (len(SIZES), LONG, terms), device="cuda", generator=g, dtype=torch.int16).to(torch.int8)
-    sx, sb = torch.rand(R, device="cuda", generator=g), torch.rand(len(SIZES), LONG, device="cuda", generator=g)
+    b = torch.randint(-127, 128, (len(SIZES), cols, terms), device="cuda", generator=g, dtype=torch.int16).to(torch.int8)
+    sx, sb = torch.rand(R, device="cuda", generator=g), torch.rand(len(SIZES), cols, device="cuda", generator=g)
     row, w = _rows(g, n, R), torch.randn(n, device="cuda", generator=g)
-    out = torch.full((n + 2, LONG), 5.0, device="cuda", dtype=dtype)
-    epdc.epdc_expert_linear_int(len(SIZES), LONG, terms, n, R, x, sx, off, row, w, b, sb, out, KIND[dtype])
+    out = torch.full((n + 2, cols), 5.0, device="cuda", dtype=dtype)
+    epdc.epdc_expert_linear_int(len(SIZES), cols, terms, n, R, x, sx, off, row, w, b, sb, out, KIND[dtype])
     ref, _ = O.product(x, o, row, w, b, n, out, sx, sb)
     _check(out, ref, O.int8_bound(ref, dtype), terms)
     assert (out[n:] == 5).all()
