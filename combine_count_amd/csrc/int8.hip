@@ -6,7 +6,8 @@
 //
 // Bound by memory.  A wave (short rows) or a block takes a row; its first
 // elements stay in registers between the maximum and the codes, what is beyond
-// them is read again (out of the cache).
+// them is read again (out of the cache).  32768 x 7168 bf16: 139 us, 5.1 TB/s; the
+// activation's 32768 x 2048 117 us, instructions (2.9 TB/s).
 //
 // The activation's codes are those of its values in 64 bits.  A 32-bit value a
 // of it is within 2^-20 |a|: where a / scale is that near the border between
