@@ -22,7 +22,9 @@ int check_type(const char *name, int32_t dtype) {
 
 int check_groups(int32_t numExperts, int32_t maxEntries) {
     if (numExperts < 1 || numExperts > 65535) return fail(EPDC_ERR_INVALID_ARG, "numExperts %d outside [1, 65535]", numExperts);
-    if (maxEntries < 0) return fail(EPDC_ERR_INVALID_ARG, "maxEntries %d < 0", maxEntries);
+    // (a group's length rounded up to whole tiles is an int32)
+    if (maxEntries < 0 || maxEntries > EPDC_MAX_EXPERT_ENTRIES)
+        return fail(EPDC_ERR_INVALID_ARG, "maxEntries %d outside [0, %d]", maxEntries, EPDC_MAX_EXPERT_ENTRIES);
     return EPDC_OK;
 }
 

@@ -12,6 +12,9 @@ struct Eight {
     float v[8];
 };
 
+// A grid's threads are counted in 32 bits: beyond this many blocks of 256 they go on to further rows.
+constexpr int64_t kMostBlocks = 1 << 23;
+
 // Eight elements on the way: 16 bytes of bf16, 32 of fp32.
 template <bool FP32>
 struct Raw8 {

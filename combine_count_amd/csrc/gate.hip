@@ -20,7 +20,7 @@ template <bool FP32, bool OUT32>
 __global__ __launch_bounds__(256) void gate_kernel(GateParams P, DivMagic rowDiv) {
     const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
     const uint32_t perRow = P.F / 8;
-    const int64_t at = (int64_t)blockIdx.x * (256 * kUnits);
+    for (int64_t at = (int64_t)blockIdx.x * (256 * kUnits);; at += (int64_t)gridDim.x * (256 * kUnits)) {
     const int64_t blockRow = at / perRow;
     const uint32_t blockUnit = (uint32_t)(at - blockRow * perRow);
     if (blockRow >= rows.last) return;
@@ -49,15 +49,17 @@ __global__ __launch_bounds__(256) void gate_kernel(GateParams P, DivMagic rowDiv
         for (int j = 0; j < 8; ++j) a.v[j] = gv.v[j] * sigmoid_of(gv.v[j]).s * uv.v[j] * w[i];
         store_eight<OUT32>(P.out + (int64_t)row[i] * P.F * (OUT32 ? 4 : 2), unit[i], a);
     }
+    }
 }
 
 template <bool FP32, bool OUT32, int TEAM>
 __global__ __launch_bounds__(256) void gate_grad_kernel(GateParams P) {
     __shared__ float part[4];
     const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
-    const int32_t row = (int32_t)(blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM);
-    if (row < rows.first || row >= rows.last) return;  // the whole team
     const int32_t lane = threadIdx.x % TEAM, perRow = P.F / 8;
+    for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < rows.last;
+         row += (int64_t)gridDim.x * (256 / TEAM)) {
+    if (row < rows.first) continue;  // the whole team
     const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4), *d = P.dOut + (int64_t)row * P.F * (OUT32 ? 4 : 2);
     uint8_t *out = P.out + (int64_t)row * P.F * (FP32 ? 8 : 4);
     const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
@@ -78,18 +80,18 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateParams P) {
         store_eight<FP32>(out, unit, dg);
         store_eight<FP32>(out, perRow + unit, du);
     }
-    if (!P.perEntry) return;
+    if (!P.perEntry) continue;
     sum = team_sum<TEAM>(sum, part);
     if (lane == 0) P.perEntry[row] = sum;
+    }
 }
 
 }  // namespace
 
 hipError_t launch_gate(const GateParams &P, bool fp32, bool out32, hipStream_t stream) {
     const int64_t blocks = ((int64_t)P.maxEntries * (P.F / 8) + 256 * kUnits - 1) / (256 * kUnits);
-    if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
     const DivMagic div = div_magic((uint32_t)P.F / 8);
-    const dim3 grid((uint32_t)blocks);
+    const dim3 grid((uint32_t)min(blocks, kMostBlocks));
     if (fp32 && out32)
         hipLaunchKernelGGL((gate_kernel<true, true>), grid, dim3(256), 0, stream, P, div);
     else if (fp32)
@@ -105,7 +107,7 @@ namespace {
 
 template <int TEAM>
 hipError_t launch_gate_grad_team(const GateParams &P, bool fp32, bool out32, hipStream_t stream) {
-    const dim3 grid((uint32_t)ceil_div(P.maxEntries, 256 / TEAM));
+    const dim3 grid((uint32_t)min((int64_t)ceil_div(P.maxEntries, 256 / TEAM), kMostBlocks));
     if (fp32 && out32)
         hipLaunchKernelGGL((gate_grad_kernel<true, true, TEAM>), grid, dim3(256), 0, stream, P);
     else if (fp32)

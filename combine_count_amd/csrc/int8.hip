@@ -45,13 +45,13 @@ __device__ __forceinline__ float scale_of(uint32_t most) {
 template <bool FP32, int TEAM, int KEEP>
 __global__ __launch_bounds__(256) void int_quantize_kernel(Int8Params P, DivMagic winDiv) {
     __shared__ uint32_t part[4];
-    const uint32_t row = blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM;
-    if (row >= P.rows) return;
-    if (P.rowCount) {
-        const uint32_t w = div_by(row, winDiv);
-        if ((int32_t)(row - w * (uint32_t)P.M) >= P.rowCount[w]) return;
-    }
     const int32_t lane = threadIdx.x % TEAM, units = P.cols / 8;
+    for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < P.rows;
+         row += (int64_t)gridDim.x * (256 / TEAM)) {
+    if (P.rowCount) {
+        const uint32_t w = div_by((uint32_t)row, winDiv);
+        if ((int32_t)((uint32_t)row - w * (uint32_t)P.M) >= P.rowCount[w]) continue;
+    }
     const uint8_t *x = P.x + (int64_t)row * P.cols * (FP32 ? 4 : 2);
     uint8_t *q = P.q + (int64_t)row * P.cols;
     Raw8<FP32> kept[KEEP];
@@ -84,6 +84,7 @@ __global__ __launch_bounds__(256) void int_quantize_kernel(Int8Params P, DivMagi
     for (int i = 0; i < KEEP; ++i)
         if (lane + i * TEAM < units) codes(to_eight<FP32>(kept[i]), lane + i * TEAM);
     for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) codes(to_eight<FP32>(load_raw8<FP32>(x, unit)), unit);
+    }
 }
 
 // The activation's value, in 64 bits, rounded to fp32.  Out of line: few lanes get here.
@@ -106,9 +107,10 @@ template <bool FP32, int TEAM>
 __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
     __shared__ uint32_t part[4];
     const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
-    const int32_t row = (int32_t)(blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM);
-    if (row < rows.first || row >= rows.last) return;
     const int32_t lane = threadIdx.x % TEAM, units = P.F / 8;
+    for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < rows.last;
+         row += (int64_t)gridDim.x * (256 / TEAM)) {
+    if (row < rows.first) continue;
     const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4);
     const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
     struct Unit {
@@ -171,6 +173,7 @@ __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
         });
         store_codes(P.out + (int64_t)row * P.F, unit, c);
     });
+    }
 }
 
 }  // namespace
@@ -178,7 +181,7 @@ __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
 hipError_t launch_int_quantize(const Int8Params &P, bool fp32, hipStream_t stream) {
     const DivMagic div = div_magic((uint32_t)P.M);
     const bool wave = P.cols <= 1024;
-    const dim3 grid((uint32_t)(wave ? (P.rows + 3) / 4 : P.rows));
+    const dim3 grid((uint32_t)min(wave ? (P.rows + 3) / 4 : P.rows, kMostBlocks));
     if (wave && fp32)
         hipLaunchKernelGGL((int_quantize_kernel<true, 64, 2>), grid, dim3(256), 0, stream, P, div);
     else if (wave)
@@ -192,7 +195,7 @@ hipError_t launch_int_quantize(const Int8Params &P, bool fp32, hipStream_t strea
 
 hipError_t launch_gate_int(const GateParams &P, bool fp32, hipStream_t stream) {
     const bool wave = P.F <= 512;
-    const dim3 grid((uint32_t)(wave ? ceil_div(P.maxEntries, 4) : P.maxEntries));
+    const dim3 grid((uint32_t)min((int64_t)(wave ? ceil_div(P.maxEntries, 4) : P.maxEntries), kMostBlocks));
     if (wave && fp32)
         hipLaunchKernelGGL((gate_int_kernel<true, 64>), grid, dim3(256), 0, stream, P);
     else if (wave)

@@ -529,6 +529,8 @@ int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, 
 
 /* Largest hiddenDim of the calls below, and largest cols of an activation. */
 #define EPDC_MAX_EXPERT_DIM 131056
+/* Largest maxEntries of the calls below. */
+#define EPDC_MAX_EXPERT_ENTRIES 2147418112
 
 /*
  * out[i] = w_i * (rows[r_i] . weights[e]^T) for every entry i of every group e.

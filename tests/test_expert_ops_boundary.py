@@ -27,6 +27,7 @@ SHARED = [
     ("no columns", dict(N=0), -1),
     ("too many columns", dict(N=(1 << 20) + 16), -1),
     ("negative entries", dict(n=-1), -1),
+    ("entries beyond the limit", dict(n=2 ** 31 - 1), -1),
     ("negative rows", dict(R=-1), -1),
     ("hidden 100", dict(H=100), -4),
     ("columns 12 in bf16", dict(N=12), -4),
@@ -134,7 +135,8 @@ def _gate_int8(v):
 
 @pytest.mark.parametrize("what,over,code", [
     ("no experts", dict(E=0), -1), ("no columns", dict(F=0), -1), ("too many columns", dict(F=131072), -1),
-    ("negative entries", dict(n=-1), -1), ("columns 12", dict(F=12), -4), ("fp8", dict(dtype=2), -2), ("type -1", dict(dtype=-1), -2),
+    ("negative entries", dict(n=-1), -1), ("entries beyond the limit", dict(n=2 ** 31 - 65535), -1),
+    ("columns 12", dict(F=12), -4), ("fp8", dict(dtype=2), -2), ("type -1", dict(dtype=-1), -2),
     ("h misaligned", dict(h=P16 + 8), -4), ("out misaligned", dict(out=P16 + 8), -4), ("offsets misaligned", dict(offsets=P16 + 2), -4),
     ("weights misaligned", dict(w=P16 + 2), -4), ("h null", dict(h=None), -5), ("out null", dict(out=None), -5),
 ])

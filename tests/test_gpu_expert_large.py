@@ -160,3 +160,27 @@ def test_no_rows_at_all():
     epdc.epdc_expert_weights_grad(E, cols, h, 0, n, d, None, n, torch.randn(n, h, device="cuda").to(BF16), None, off, None, dw,
                                   epdc.EPDC_FP32)
     assert torch.equal(dw, torch.zeros_like(dw))
+
+
+def test_more_rows_than_a_grid_has_blocks():
+    """Rows beyond 2^23 blocks of four: the blocks go on to them."""
+    n, last, cols = 34_000_001, 50, 16
+    g = _gen(6)
+    x = torch.zeros(n, cols, device="cuda", dtype=BF16)
+    x[-last:] = torch.randn(last, cols, device="cuda", generator=g)
+    x[:last] = torch.randn(last, cols, device="cuda", generator=g)
+    q, s = torch.full((n, cols), 7, device="cuda", dtype=torch.int8), torch.full((n,), 5.0, device="cuda")
+    epdc.epdc_int_quantize(1, n, cols, epdc.EPDC_BF16, x, None, q, s)
+    for part in (slice(0, last), slice(n - last, n)):
+        rq, rs = O.int8_rows(x[part])
+        assert torch.equal(q[part].cpu(), rq) and torch.equal(s[part].cpu(), rs)
+    assert (q[last:-last] == 0).all() and (s[last:-last] == 0).all()
+    # the same array as rows of two halves of eight
+    d, dh, dw = torch.ones(n, 8, device="cuda", dtype=BF16), torch.full_like(x, 5.0), torch.full((n,), 5.0, device="cuda")
+    epdc.epdc_expert_gate_grad(1, 8, n, epdc.EPDC_BF16, x, None, None, d, epdc.EPDC_BF16, dh, dw)
+    for part in (slice(0, last), slice(n - last, n)):
+        rh, rw, size, size_w = O.gate_grad(x[part], None, d[part])
+        bh, bw = O.gate_grad_bounds(x[part], rh, rw, size, size_w, BF16)
+        _near(dh[part], rh, bh)
+        _near(dw[part], rw, bw)
+    assert (dh[last:-last] == 0).all() and (dw[last:-last] == 0).all()
