@@ -331,9 +331,10 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
         next = find(b);
         if constexpr (KIND != kDenseWeightsGrad) fetch_entry(next);
     };
-    // What the requests of step kq of tile Q need.
+    // What the requests of step kq of tile Q need.  A step is one of its tile's, or (of a tile that does not exist) 0 or 1:
+    // the weights' gradient's, of 64 entries each, go up to 2^25.
     auto advance = [&] {
-        const int32_t k = uniform(min(kq, 1 << 22));
+        const int32_t k = uniform(kq);
         if constexpr (KIND != kDenseWeightsGrad) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -392,7 +393,7 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
             load_lds16_unseen<I * 1024>(stepBase, colo[I] + placeC[I & 1], to);
         } else {
             constexpr int S = BN == 256 ? (I & 1) | (I >> 2) << 1 : 0;
-            const int32_t left = P.N - 1 - uniform(min(kq, 1 << 22)) * 64 - wave * 16 - I * kPerC;  // rows behind the load's first
+            const int32_t left = P.N - 1 - uniform(kq) * 64 - wave * 16 - I * kPerC;  // rows behind the load's first
             if (!rarely(left < kPerC - 1))
                 load_lds16_unseen<I * 1024>(uniform_pointer(stepBase + (int64_t)(I * kPerC) * ((uint32_t)P.H * 2)), turnedC[S], to);
             else  // the last row, where this lane's is behind it
