@@ -75,3 +75,10 @@ def test_the_gpu_tests_reach_every_form(plan):
         # ninety experts of larger weights are tiles enough for the next form
         want = {PRODUCT: {"stream16", "stream64", "tiles128"}, ROWS: {"tiles128"}, WEIGHTS: {"tiles128", "tiles256"}}
         assert set(plan(small).values()) == want[kind]
+
+
+def test_the_streamed_shapes_reach_their_forms(plan):
+    import test_gpu_expert_stream as F
+    shapes = F.shapes()
+    got = plan([s[1:] for s in shapes])
+    assert all(got[s[1:]] == s[0] for s in shapes)
