@@ -82,3 +82,11 @@ def test_the_streamed_shapes_reach_their_forms(plan):
     shapes = F.shapes()
     got = plan([s[1:] for s in shapes])
     assert all(got[s[1:]] == s[0] for s in shapes)
+
+
+def test_the_shapes_of_many_tiles_reach_the_tiles_of_128(plan):
+    import test_gpu_expert_many_tiles as F
+    shapes = F.shapes()
+    got = plan([s[1:] for s in shapes])
+    assert all(got[s[1:]] == s[0] for s in shapes)
+    assert F.tiles() > 2.5 * F.BLOCKS
