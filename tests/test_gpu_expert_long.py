@@ -68,3 +68,20 @@ def test_weights_grad_of_gathered_entries_beyond_2_28():
     o, r = out_row[at].long(), row[at].long()
     there = (o < rows) & (r >= 0) & (r < rows)
     assert torch.equal(out[0].double(), _product(d[o[there]], x[r[there]]))
+
+
+def test_gate_int_of_more_rows_than_a_grid_has_blocks():
+    """Rows beyond 2^23 blocks of four: the blocks go on to them."""
+    import expert_oracle as O
+    n, last, cols = 34_000_001, 50, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    h = torch.zeros(n, 2 * cols, device="cuda", dtype=BF16)
+    for part in (slice(0, last), slice(n - last, n)):
+        h[part] = 2 * torch.randn(last, 2 * cols, device="cuda", generator=g)
+    q, s = torch.full((n, cols), 7, device="cuda", dtype=torch.int8), torch.full((n,), 5.0, device="cuda")
+    epdc.epdc_expert_gate_int(1, cols, n, epdc.EPDC_BF16, h, None, None, q, s)
+    for part in (slice(0, last), slice(n - last, n)):
+        rq, rs = O.int8_rows(O.gate(h[part], None).float())
+        assert torch.equal(q[part].cpu(), rq) and torch.equal(s[part].cpu(), rs)
+    assert (q[last:-last] == 0).all() and (s[last:-last] == 0).all()
