@@ -6,9 +6,9 @@ with their gradients.
 The compute path is libepdc.so (hand-written HIP for gfx950) behind the C
 ABI in include/epdc.h; this package is its Python binding.
 """
-from .binding import (EPDC_BF16, EPDC_FP4X2, EPDC_FP8, EPDC_FP32, EPDC_MAX_EXPERT_DIM, EPDC_MAX_GROUP_EXPERTS,
-                      EPDC_MAX_ROUTE_EXPERTS, EPDC_MAX_SCALE_DIM, EPDC_SIGMOID, EPDC_SOFTMAX, EPDC_STATUS_ROW_OUTSIDE,
-                      EPDC_STATUS_WAIT_TIMEOUT, EPDC_STATUS_WORD, EXPORTS, EpCfg, EpdcError, PreparedCall, RouteCfg,
+from .binding import (EPDC_BF16, EPDC_FP4X2, EPDC_FP8, EPDC_FP32, EPDC_MAX_EXPERT_DIM, EPDC_MAX_EXPERT_ENTRIES,
+                      EPDC_MAX_GROUP_EXPERTS, EPDC_MAX_ROUTE_EXPERTS, EPDC_MAX_SCALE_DIM, EPDC_SIGMOID, EPDC_SOFTMAX,
+                      EPDC_STATUS_ROW_OUTSIDE, EPDC_STATUS_WAIT_TIMEOUT, EPDC_STATUS_WORD, EXPORTS, EpCfg, EpdcError, PreparedCall, RouteCfg,
                       dispatch_status, epdc_combine, epdc_combine_push, epdc_combine_reduce, epdc_dispatch,
                       epdc_dispatch_noalloc,
                       epdc_dispatch_scratch_bytes, epdc_landing_rows, epdc_last_error, load_library,
@@ -34,7 +34,8 @@ __all__ = ["EPDC_BF16", "EPDC_FP32", "EPDC_FP8", "EPDC_FP4X2", "EPDC_MAX_SCALE_D
            "epdc_route", "epdc_route_grad", "epdc_mx_scale_dim", "epdc_mx_quantize", "epdc_mx_dequantize",
            "epdc_group_scratch_bytes", "epdc_group_experts", "epdc_expert_product", "prepare_route",
            "prepare_route_grad", "prepare_mx_quantize", "prepare_mx_dequantize", "prepare_group_experts",
-           "prepare_expert_product", "EPDC_MAX_EXPERT_DIM", "epdc_expert_linear", "epdc_expert_rows_grad",
+           "prepare_expert_product", "EPDC_MAX_EXPERT_DIM", "EPDC_MAX_EXPERT_ENTRIES",
+           "epdc_expert_linear", "epdc_expert_rows_grad",
            "epdc_expert_weights_grad", "epdc_expert_gate", "epdc_expert_gate_grad", "epdc_int_quantize",
            "epdc_expert_gate_int", "epdc_expert_linear_int", "prepare_expert_linear",
            "prepare_expert_rows_grad", "prepare_expert_weights_grad", "prepare_expert_gate",

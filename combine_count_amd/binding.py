@@ -40,6 +40,7 @@ EPDC_SOFTMAX, EPDC_SIGMOID = 0, 1
 EPDC_MAX_ROUTE_EXPERTS = 1024
 EPDC_MAX_GROUP_EXPERTS = 1024
 EPDC_MAX_EXPERT_DIM = 131056
+EPDC_MAX_EXPERT_ENTRIES = 2147418112
 
 
 class EpdcError(RuntimeError):

@@ -180,3 +180,15 @@ def test_host_tensors_and_wide_integers_are_refused():
         epdc.epdc_expert_linear(1, 64, 64, 64, 64, t, P16, None, None, P16, P16, epdc.EPDC_BF16, stream=0)
     with pytest.raises(ValueError, match="32 bits"):
         epdc.epdc_expert_gate(1, 32, 1 << 31, epdc.EPDC_BF16, P16, None, None, P16, epdc.EPDC_BF16, stream=0)
+
+
+def test_the_largest_number_of_entries():
+    src = open(os.path.join(ROOT, "include", "epdc.h")).read()
+    limit = epdc.EPDC_MAX_EXPERT_ENTRIES
+    assert int(re.search(r"EPDC_MAX_EXPERT_ENTRIES (\d+)", src).group(1)) == limit
+    assert "EPDC_MAX_EXPERT_ENTRIES" in epdc.__all__
+    for call in (_product, _rows_grad, _int8):  # the limit itself passes this check and meets the next
+        assert call({**PRODUCT, "n": limit + 1}) == -1 and call({**PRODUCT, "n": limit, "x": None}) == -5
+    for call in (_gate, _gate_grad, _gate_int8):
+        assert call({**GATE, "n": limit + 1}) == -1 and call({**GATE, "n": limit, "h": None}) == -5
+    assert _weights_grad({**GRAD, "n": limit + 1}) == -1 and _weights_grad({**GRAD, "n": limit, "d": None}) == -5
