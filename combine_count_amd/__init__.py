@@ -8,11 +8,11 @@ ABI in include/epdc.h; this package is its Python binding.
 """
 from .binding import (EPDC_BF16, EPDC_FP4X2, EPDC_FP8, EPDC_FP32, EPDC_MAX_EXPERT_DIM, EPDC_MAX_EXPERT_ENTRIES,
                       EPDC_MAX_GROUP_EXPERTS, EPDC_MAX_ROUTE_EXPERTS, EPDC_MAX_SCALE_DIM, EPDC_SIGMOID, EPDC_SOFTMAX,
-                      EPDC_STATUS_ROW_OUTSIDE, EPDC_STATUS_WAIT_TIMEOUT, EPDC_STATUS_WORD, EXPORTS, EpCfg, EpdcError, PreparedCall, RouteCfg,
-                      dispatch_status, epdc_combine, epdc_combine_push, epdc_combine_reduce, epdc_dispatch,
-                      epdc_dispatch_noalloc,
-                      epdc_dispatch_scratch_bytes, epdc_landing_rows, epdc_last_error, load_library,
-                      prepare_combine, prepare_combine_push, prepare_combine_reduce, prepare_dispatch)
+                      EPDC_STATUS_ROW_OUTSIDE, EPDC_STATUS_WAIT_TIMEOUT, EPDC_STATUS_WORD, EXPORTS, EpCfg, EpdcError,
+                      PreparedCall, RouteCfg, dispatch_status, epdc_combine, epdc_combine_push, epdc_combine_reduce,
+                      epdc_dispatch, epdc_dispatch_noalloc, epdc_dispatch_scratch_bytes, epdc_landing_rows,
+                      epdc_last_error, load_library, prepare_combine, prepare_combine_push, prepare_combine_reduce,
+                      prepare_dispatch)
 from .buffers import DispatchBuffers, LandingBuffers
 from .expert_ops import (epdc_expert_gate, epdc_expert_gate_grad, epdc_expert_gate_int, epdc_expert_linear,
                          epdc_expert_linear_int, epdc_expert_rows_grad, epdc_expert_weights_grad, epdc_int_quantize,

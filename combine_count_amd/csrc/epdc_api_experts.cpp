@@ -99,8 +99,8 @@ int gate_params(int32_t numExperts, int32_t cols, int32_t maxEntries, const void
 extern "C" {
 
 int epdc_expert_linear(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries, int32_t numRows,
-                             const void *rows, const int32_t *offsets, const int32_t *entryRow, const float *entryWeight,
-                             const void *weights, void *out, int32_t outDtype, void *stream) {
+                       const void *rows, const int32_t *offsets, const int32_t *entryRow, const float *entryWeight,
+                       const void *weights, void *out, int32_t outDtype, void *stream) {
     try {
         g_lastError.clear();
         int rc = check_product(numExperts, numCols, hiddenDim, maxEntries, numRows, outDtype, 16 / size_of(outDtype), 8);
@@ -109,8 +109,8 @@ int epdc_expert_linear(int32_t numExperts, int32_t numCols, int32_t hiddenDim, i
         rc = product_params(numExperts, numCols, hiddenDim, maxEntries, numRows, rows, offsets, entryRow, entryWeight, weights,
                             out, P);
         if (rc != EPDC_OK) return rc;
-        return hip_status(epdc::launch_dense_linear(P, epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries), outDtype == EPDC_FP32,
-                                             static_cast<hipStream_t>(stream)),
+        const epdc::DenseForm form = epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries);
+        return hip_status(epdc::launch_dense_linear(P, form, outDtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
                           "bf16 product launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_linear");
@@ -128,8 +128,8 @@ int epdc_expert_rows_grad(int32_t numExperts, int32_t numCols, int32_t hiddenDim
         rc = product_params(numExperts, numCols, hiddenDim, maxEntries, numRows, dOut, offsets, entryRow, entryWeight, weights,
                             dRows, P);
         if (rc != EPDC_OK) return rc;
-        return hip_status(epdc::launch_dense_rows_grad(P, epdc::plan_dense(epdc::kDenseRowsGrad, P.E, P.N, P.H, P.maxEntries), dtype == EPDC_FP32,
-                                             static_cast<hipStream_t>(stream)),
+        const epdc::DenseForm form = epdc::plan_dense(epdc::kDenseRowsGrad, P.E, P.N, P.H, P.maxEntries);
+        return hip_status(epdc::launch_dense_rows_grad(P, form, dtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
                           "rows' gradient launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_rows_grad");
@@ -167,8 +167,8 @@ int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hidden
         P.outRow = outRow;
         P.base = static_cast<const uint8_t *>(base);
         P.out = static_cast<uint8_t *>(dWeights);
-        return hip_status(epdc::launch_dense_weights_grad(P, epdc::plan_dense(epdc::kDenseWeightsGrad, P.E, P.N, P.H, P.maxEntries), dtype == EPDC_FP32,
-                                             static_cast<hipStream_t>(stream)),
+        const epdc::DenseForm form = epdc::plan_dense(epdc::kDenseWeightsGrad, P.E, P.N, P.H, P.maxEntries);
+        return hip_status(epdc::launch_dense_weights_grad(P, form, dtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
                           "weights' gradient launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_weights_grad");
@@ -176,9 +176,9 @@ int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hidden
 }
 
 int epdc_expert_linear_int(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries, int32_t numRows,
-                             const void *rows, const float *rowScales, const int32_t *offsets, const int32_t *entryRow,
-                             const float *entryWeight, const void *weights, const float *weightScales, void *out,
-                             int32_t outDtype, void *stream) {
+                           const void *rows, const float *rowScales, const int32_t *offsets, const int32_t *entryRow,
+                           const float *entryWeight, const void *weights, const float *weightScales, void *out,
+                           int32_t outDtype, void *stream) {
     try {
         g_lastError.clear();
         int rc = check_product(numExperts, numCols, hiddenDim, maxEntries, numRows, outDtype, 16 / size_of(outDtype), 16);
@@ -192,8 +192,8 @@ int epdc_expert_linear_int(int32_t numExperts, int32_t numCols, int32_t hiddenDi
             return fail(EPDC_ERR_ALIGN, "rowScales and weightScales must be 4-byte aligned");
         P.rowScales = rowScales;
         P.weightScales = weightScales;
-        return hip_status(epdc::launch_dense_linear_int(P, epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries), outDtype == EPDC_FP32,
-                                             static_cast<hipStream_t>(stream)),
+        const epdc::DenseForm form = epdc::plan_dense(epdc::kDenseProduct, P.E, P.N, P.H, P.maxEntries);
+        return hip_status(epdc::launch_dense_linear_int(P, form, outDtype == EPDC_FP32, static_cast<hipStream_t>(stream)),
                           "int8 product launch");
     } catch (...) {
         return fail(EPDC_ERR_HIP, "unexpected C++ exception in epdc_expert_linear_int");
@@ -239,7 +239,7 @@ int epdc_expert_gate_grad(int32_t numExperts, int32_t cols, int32_t maxEntries, 
 }
 
 int epdc_expert_gate_int(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
-                          const int32_t *offsets, const float *entryWeight, void *q, float *scales, void *stream) {
+                         const int32_t *offsets, const float *entryWeight, void *q, float *scales, void *stream) {
     try {
         g_lastError.clear();
         int rc = check_gate(numExperts, cols, maxEntries, dtype, 16);
@@ -255,7 +255,7 @@ int epdc_expert_gate_int(int32_t numExperts, int32_t cols, int32_t maxEntries, i
 }
 
 int epdc_int_quantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, int32_t dtype, const void *x,
-                       const int32_t *rowCount, void *q, float *scales, void *stream) {
+                      const int32_t *rowCount, void *q, float *scales, void *stream) {
     try {
         g_lastError.clear();
         if (numWindows < 0 || rowsPerWindow < 0)

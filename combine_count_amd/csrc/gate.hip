@@ -21,34 +21,34 @@ __global__ __launch_bounds__(256) void gate_kernel(GateParams P, DivMagic rowDiv
     const RowRange rows = rows_of_groups(P.offsets, P.E, P.maxEntries);
     const uint32_t perRow = P.F / 8;
     for (int64_t at = (int64_t)blockIdx.x * (256 * kUnits);; at += (int64_t)gridDim.x * (256 * kUnits)) {
-    const int64_t blockRow = at / perRow;
-    const uint32_t blockUnit = (uint32_t)(at - blockRow * perRow);
-    if (blockRow >= rows.last) return;
-    Raw8<FP32> g[kUnits], u[kUnits];
-    int32_t row[kUnits], unit[kUnits];
-    float w[kUnits];
-    bool live[kUnits];
+        const int64_t blockRow = at / perRow;
+        const uint32_t blockUnit = (uint32_t)(at - blockRow * perRow);
+        if (blockRow >= rows.last) return;
+        Raw8<FP32> g[kUnits], u[kUnits];
+        int32_t row[kUnits], unit[kUnits];
+        float w[kUnits];
+        bool live[kUnits];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const uint32_t n = blockUnit + i * 256 + threadIdx.x, r = div_by(n, rowDiv);
-        row[i] = (int32_t)min(blockRow + r, (int64_t)INT32_MAX);
-        unit[i] = (int32_t)(n - r * perRow);
-        live[i] = row[i] >= rows.first && row[i] < rows.last;
-        if (!live[i]) continue;
-        const uint8_t *h = P.h + (int64_t)row[i] * P.F * (FP32 ? 8 : 4);
-        g[i] = load_raw8<FP32>(h, unit[i]);
-        u[i] = load_raw8<FP32>(h, perRow + unit[i]);
-        w[i] = P.entryWeight ? P.entryWeight[row[i]] : 1.0f;
-    }
+        for (int i = 0; i < kUnits; ++i) {
+            const uint32_t n = blockUnit + i * 256 + threadIdx.x, r = div_by(n, rowDiv);
+            row[i] = (int32_t)min(blockRow + r, (int64_t)INT32_MAX);
+            unit[i] = (int32_t)(n - r * perRow);
+            live[i] = row[i] >= rows.first && row[i] < rows.last;
+            if (!live[i]) continue;
+            const uint8_t *h = P.h + (int64_t)row[i] * P.F * (FP32 ? 8 : 4);
+            g[i] = load_raw8<FP32>(h, unit[i]);
+            u[i] = load_raw8<FP32>(h, perRow + unit[i]);
+            w[i] = P.entryWeight ? P.entryWeight[row[i]] : 1.0f;
+        }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        if (!live[i]) continue;
-        const Eight gv = to_eight<FP32>(g[i]), uv = to_eight<FP32>(u[i]);
-        Eight a;
+        for (int i = 0; i < kUnits; ++i) {
+            if (!live[i]) continue;
+            const Eight gv = to_eight<FP32>(g[i]), uv = to_eight<FP32>(u[i]);
+            Eight a;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a.v[j] = gv.v[j] * sigmoid_of(gv.v[j]).s * uv.v[j] * w[i];
-        store_eight<OUT32>(P.out + (int64_t)row[i] * P.F * (OUT32 ? 4 : 2), unit[i], a);
-    }
+            for (int j = 0; j < 8; ++j) a.v[j] = gv.v[j] * sigmoid_of(gv.v[j]).s * uv.v[j] * w[i];
+            store_eight<OUT32>(P.out + (int64_t)row[i] * P.F * (OUT32 ? 4 : 2), unit[i], a);
+        }
     }
 }
 
@@ -59,30 +59,30 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateParams P) {
     const int32_t lane = threadIdx.x % TEAM, perRow = P.F / 8;
     for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < rows.last;
          row += (int64_t)gridDim.x * (256 / TEAM)) {
-    if (row < rows.first) continue;  // the whole team
-    const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4), *d = P.dOut + (int64_t)row * P.F * (OUT32 ? 4 : 2);
-    uint8_t *out = P.out + (int64_t)row * P.F * (FP32 ? 8 : 4);
-    const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
-    float sum = 0.0f;
-    for (int32_t unit = lane; unit < perRow; unit += TEAM) {
-        const Raw8<FP32> graw = load_raw8<FP32>(h, unit), uraw = load_raw8<FP32>(h, perRow + unit);
-        const Raw8<OUT32> draw = load_raw8<OUT32>(d, unit);
-        const Eight g = to_eight<FP32>(graw), u = to_eight<FP32>(uraw), da = to_eight<OUT32>(draw);
-        Eight dg, du;
+        if (row < rows.first) continue;  // the whole team
+        const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4), *d = P.dOut + (int64_t)row * P.F * (OUT32 ? 4 : 2);
+        uint8_t *out = P.out + (int64_t)row * P.F * (FP32 ? 8 : 4);
+        const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
+        float sum = 0.0f;
+        for (int32_t unit = lane; unit < perRow; unit += TEAM) {
+            const Raw8<FP32> graw = load_raw8<FP32>(h, unit), uraw = load_raw8<FP32>(h, perRow + unit);
+            const Raw8<OUT32> draw = load_raw8<OUT32>(d, unit);
+            const Eight g = to_eight<FP32>(graw), u = to_eight<FP32>(uraw), da = to_eight<OUT32>(draw);
+            Eight dg, du;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const Sigmoid s = sigmoid_of(g.v[j]);
-            const float gs = g.v[j] * s.s;
-            sum = fmaf(da.v[j] * gs, u.v[j], sum);
-            dg.v[j] = da.v[j] * w * u.v[j] * (s.s * fmaf(g.v[j], s.rest, 1.0f));
-            du.v[j] = da.v[j] * w * gs;
+            for (int j = 0; j < 8; ++j) {
+                const Sigmoid s = sigmoid_of(g.v[j]);
+                const float gs = g.v[j] * s.s;
+                sum = fmaf(da.v[j] * gs, u.v[j], sum);
+                dg.v[j] = da.v[j] * w * u.v[j] * (s.s * fmaf(g.v[j], s.rest, 1.0f));
+                du.v[j] = da.v[j] * w * gs;
+            }
+            store_eight<FP32>(out, unit, dg);
+            store_eight<FP32>(out, perRow + unit, du);
         }
-        store_eight<FP32>(out, unit, dg);
-        store_eight<FP32>(out, perRow + unit, du);
-    }
-    if (!P.perEntry) continue;
-    sum = team_sum<TEAM>(sum, part);
-    if (lane == 0) P.perEntry[row] = sum;
+        if (!P.perEntry) continue;
+        sum = team_sum<TEAM>(sum, part);
+        if (lane == 0) P.perEntry[row] = sum;
     }
 }
 

@@ -48,42 +48,42 @@ __global__ __launch_bounds__(256) void int_quantize_kernel(Int8Params P, DivMagi
     const int32_t lane = threadIdx.x % TEAM, units = P.cols / 8;
     for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < P.rows;
          row += (int64_t)gridDim.x * (256 / TEAM)) {
-    if (P.rowCount) {
-        const uint32_t w = div_by((uint32_t)row, winDiv);
-        if ((int32_t)((uint32_t)row - w * (uint32_t)P.M) >= P.rowCount[w]) continue;
-    }
-    const uint8_t *x = P.x + (int64_t)row * P.cols * (FP32 ? 4 : 2);
-    uint8_t *q = P.q + (int64_t)row * P.cols;
-    Raw8<FP32> kept[KEEP];
+        if (P.rowCount) {
+            const uint32_t w = div_by((uint32_t)row, winDiv);
+            if ((int32_t)((uint32_t)row - w * (uint32_t)P.M) >= P.rowCount[w]) continue;
+        }
+        const uint8_t *x = P.x + (int64_t)row * P.cols * (FP32 ? 4 : 2);
+        uint8_t *q = P.q + (int64_t)row * P.cols;
+        Raw8<FP32> kept[KEEP];
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-        if (lane + i * TEAM < units)
-            kept[i] = load_raw8<FP32>(x, lane + i * TEAM);
-        else
-            kept[i] = Raw8<FP32>{};
-    }
-    uint32_t most = 0;
-    auto highest = [&](const Eight &e) {
+        for (int i = 0; i < KEEP; ++i) {
+            if (lane + i * TEAM < units)
+                kept[i] = load_raw8<FP32>(x, lane + i * TEAM);
+            else
+                kept[i] = Raw8<FP32>{};
+        }
+        uint32_t most = 0;
+        auto highest = [&](const Eight &e) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most = max(most, magnitude(e.v[j]));
-    };
+            for (int j = 0; j < 8; ++j) most = max(most, magnitude(e.v[j]));
+        };
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) highest(to_eight<FP32>(kept[i]));
-    for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) highest(to_eight<FP32>(load_raw8<FP32>(x, unit)));
-    most = team_max<TEAM>(most, part);
-    const float scale = scale_of(most);
-    if (lane == 0) P.scales[row] = scale;
-    const bool none = !(scale > 0.0f);
-    auto codes = [&](const Eight &e, int32_t unit) {
-        int32_t c[8];
+        for (int i = 0; i < KEEP; ++i) highest(to_eight<FP32>(kept[i]));
+        for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) highest(to_eight<FP32>(load_raw8<FP32>(x, unit)));
+        most = team_max<TEAM>(most, part);
+        const float scale = scale_of(most);
+        if (lane == 0) P.scales[row] = scale;
+        const bool none = !(scale > 0.0f);
+        auto codes = [&](const Eight &e, int32_t unit) {
+            int32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = none ? 0 : code_of(e.v[j], scale);
-        store_codes(q, unit, c);
-    };
+            for (int j = 0; j < 8; ++j) c[j] = none ? 0 : code_of(e.v[j], scale);
+            store_codes(q, unit, c);
+        };
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i)
-        if (lane + i * TEAM < units) codes(to_eight<FP32>(kept[i]), lane + i * TEAM);
-    for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) codes(to_eight<FP32>(load_raw8<FP32>(x, unit)), unit);
+        for (int i = 0; i < KEEP; ++i)
+            if (lane + i * TEAM < units) codes(to_eight<FP32>(kept[i]), lane + i * TEAM);
+        for (int32_t unit = lane + KEEP * TEAM; unit < units; unit += TEAM) codes(to_eight<FP32>(load_raw8<FP32>(x, unit)), unit);
     }
 }
 
@@ -110,69 +110,69 @@ __global__ __launch_bounds__(256) void gate_int_kernel(GateParams P) {
     const int32_t lane = threadIdx.x % TEAM, units = P.F / 8;
     for (int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM; row < rows.last;
          row += (int64_t)gridDim.x * (256 / TEAM)) {
-    if (row < rows.first) continue;
-    const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4);
-    const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
-    struct Unit {
-        Raw8<FP32> g, u;
-        Eight a;
-    };
-    auto load = [&](int32_t unit) {
-        Unit x{load_raw8<FP32>(h, unit), load_raw8<FP32>(h, units + unit), {}};
-        const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
+        if (row < rows.first) continue;
+        const uint8_t *h = P.h + (int64_t)row * P.F * (FP32 ? 8 : 4);
+        const float w = P.entryWeight ? P.entryWeight[row] : 1.0f;
+        struct Unit {
+            Raw8<FP32> g, u;
+            Eight a;
+        };
+        auto load = [&](int32_t unit) {
+            Unit x{load_raw8<FP32>(h, unit), load_raw8<FP32>(h, units + unit), {}};
+            const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // 1 / (1 + t) to a step
-            const float t = expf(-fabsf(g.v[j])), large = __builtin_amdgcn_rcpf(1.0f + t);
-            x.a.v[j] = g.v[j] * (g.v[j] >= 0.0f ? large : t * large) * u.v[j] * w;
-        }
-        return x;
-    };
-    auto each_value = [&](const Unit &x, auto &&f) {  // f(place, value in 32 bits, g, u)
-        const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
+            for (int j = 0; j < 8; ++j) {
+                // 1 / (1 + t) to a step
+                const float t = expf(-fabsf(g.v[j])), large = __builtin_amdgcn_rcpf(1.0f + t);
+                x.a.v[j] = g.v[j] * (g.v[j] >= 0.0f ? large : t * large) * u.v[j] * w;
+            }
+            return x;
+        };
+        auto each_value = [&](const Unit &x, auto &&f) {  // f(place, value in 32 bits, g, u)
+            const Eight g = to_eight<FP32>(x.g), u = to_eight<FP32>(x.u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f(j, x.a.v[j], g.v[j], u.v[j]);
-    };
-    Unit kept{};
-    if (lane < units) kept = load(lane);
-    auto each_unit = [&](auto &&f) {
-        if (lane < units) f(kept, lane);
-        for (int32_t unit = lane + TEAM; unit < units; unit += TEAM) f(load(unit), unit);
-    };
-    uint32_t most = 0;
-    bool odd = false;  // factors beyond the bounds
-    each_unit([&](const Unit &x, int32_t) {
-        each_value(x, [&](int, float a, float, float u) {
-            most = max(most, magnitude(a));
-            odd |= !plain_factors(u, P.entryWeight ? fabsf(w) : 1.0f);
+            for (int j = 0; j < 8; ++j) f(j, x.a.v[j], g.v[j], u.v[j]);
+        };
+        Unit kept{};
+        if (lane < units) kept = load(lane);
+        auto each_unit = [&](auto &&f) {
+            if (lane < units) f(kept, lane);
+            for (int32_t unit = lane + TEAM; unit < units; unit += TEAM) f(load(unit), unit);
+        };
+        uint32_t most = 0;
+        bool odd = false;  // factors beyond the bounds
+        each_unit([&](const Unit &x, int32_t) {
+            each_value(x, [&](int, float a, float, float u) {
+                most = max(most, magnitude(a));
+                odd |= !plain_factors(u, P.entryWeight ? fabsf(w) : 1.0f);
+            });
         });
-    });
-    most = team_max<TEAM>(most, part);
-    // A row of odd factors, or of values beyond the middle of fp32's range: every value in 64 bits.
-    const bool all = team_max<TEAM>(odd, part) != 0 || !(__uint_as_float(most) > 0x1p-40f && __uint_as_float(most) < 0x1p100f);
-    const float near = __uint_as_float(most) * (1.0f - 2 * kClose);
-    most = 0;
-    each_unit([&](const Unit &x, int32_t) {
-        each_value(x, [&](int, float a, float g, float u) {
-            if (all || fabsf(a) >= near) most = max(most, magnitude(gate_exactly(g, u, w)));
+        most = team_max<TEAM>(most, part);
+        // A row of odd factors, or of values beyond the middle of fp32's range: every value in 64 bits.
+        const bool all = team_max<TEAM>(odd, part) != 0 || !(__uint_as_float(most) > 0x1p-40f && __uint_as_float(most) < 0x1p100f);
+        const float near = __uint_as_float(most) * (1.0f - 2 * kClose);
+        most = 0;
+        each_unit([&](const Unit &x, int32_t) {
+            each_value(x, [&](int, float a, float g, float u) {
+                if (all || fabsf(a) >= near) most = max(most, magnitude(gate_exactly(g, u, w)));
+            });
         });
-    });
-    most = team_max<TEAM>(most, part);
-    const float scale = scale_of(most);
-    if (lane == 0) P.perEntry[row] = scale;
-    const bool none = !(scale > 0.0f);
-    const float over = 1.0f / scale;
-    each_unit([&](const Unit &x, int32_t unit) {
-        int32_t c[8];
-        each_value(x, [&](int j, float a, float g, float u) {
-            // Far enough from the border between two codes the quotient's last bits do not count: at 127 a value's
-            // error is 2^-13 of a code, this product's another 2^-16.
-            const float q = a * over, r = rintf(q);
-            c[j] = (int32_t)fminf(fmaxf(r, -127.0f), 127.0f);
-            if (all || fabsf(fabsf(q - r) - 0.5f) < 0x1p-11f) c[j] = none ? 0 : code_of(gate_exactly(g, u, w), scale);
+        most = team_max<TEAM>(most, part);
+        const float scale = scale_of(most);
+        if (lane == 0) P.perEntry[row] = scale;
+        const bool none = !(scale > 0.0f);
+        const float over = 1.0f / scale;
+        each_unit([&](const Unit &x, int32_t unit) {
+            int32_t c[8];
+            each_value(x, [&](int j, float a, float g, float u) {
+                // Far enough from the border between two codes the quotient's last bits do not count: at 127 a value's
+                // error is 2^-13 of a code, this product's another 2^-16.
+                const float q = a * over, r = rintf(q);
+                c[j] = (int32_t)fminf(fmaxf(r, -127.0f), 127.0f);
+                if (all || fabsf(fabsf(q - r) - 0.5f) < 0x1p-11f) c[j] = none ? 0 : code_of(gate_exactly(g, u, w), scale);
+            });
+            store_codes(P.out + (int64_t)row * P.F, unit, c);
         });
-        store_codes(P.out + (int64_t)row * P.F, unit, c);
-    });
     }
 }
 

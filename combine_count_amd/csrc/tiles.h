@@ -17,7 +17,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Behind inline matrix instructions, before their sums are read.
 __device__ __forceinline__ void mfma_done() { asm volatile("s_nop 15\n\ts_nop 15"); }
 
-
 // Two values as bf16, the first low, rounded to nearest even.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
@@ -35,7 +34,6 @@ __device__ __forceinline__ void load_lds16(const uint8_t *src, uint8_t *lds) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, 0xffffffff, 0x00020000);
 }
-
 
 // Where a block's tile lies: expert, entries [m0, hi), columns from n0.
 struct TileAt {

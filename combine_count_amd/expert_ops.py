@@ -19,7 +19,7 @@ def _sizes(*values):
 
 
 def prepare_expert_linear(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, rows, offsets,
-                                entryRow, entryWeight, weights, out, outDtype: int) -> PreparedCall:
+                          entryRow, entryWeight, weights, out, outDtype: int) -> PreparedCall:
     E, N, H, n, R = _sizes(numExperts, numCols, hiddenDim, maxEntries, numRows)
     args = [_i(numExperts), _i(numCols), _i(hiddenDim), _i(maxEntries), _i(numRows), _array(rows, R * H * 2, "rows", _B),
             _array(offsets, (E + 1) * 4, "offsets", _I), _array(entryRow, n * 4, "entryRow", _I),
@@ -79,7 +79,7 @@ def prepare_int_quantize(numWindows: int, rowsPerWindow: int, cols: int, dtype: 
 
 
 def prepare_expert_gate_int(numExperts: int, cols: int, maxEntries: int, dtype: int, h, offsets, entryWeight, q,
-                             scales) -> PreparedCall:
+                            scales) -> PreparedCall:
     E, F, n = _sizes(numExperts, cols, maxEntries)
     args = [_i(numExperts), _i(cols), _i(maxEntries), _i(dtype),
             _array(h, n * 2 * F * _BYTES.get(dtype, 0), "h", _FLOATS.get(dtype)),
@@ -89,7 +89,7 @@ def prepare_expert_gate_int(numExperts: int, cols: int, maxEntries: int, dtype: 
 
 
 def prepare_expert_linear_int(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, rows, rowScales,
-                                offsets, entryRow, entryWeight, weights, weightScales, out, outDtype: int) -> PreparedCall:
+                              offsets, entryRow, entryWeight, weights, weightScales, out, outDtype: int) -> PreparedCall:
     E, N, H, n, R = _sizes(numExperts, numCols, hiddenDim, maxEntries, numRows)
     args = [_i(numExperts), _i(numCols), _i(hiddenDim), _i(maxEntries), _i(numRows), _array(rows, R * H, "rows", size=1),
             _array(rowScales, R * 4, "rowScales", _F), _array(offsets, (E + 1) * 4, "offsets", _I),
@@ -101,9 +101,9 @@ def prepare_expert_linear_int(numExperts: int, numCols: int, hiddenDim: int, max
 
 
 def epdc_expert_linear(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, rows, offsets,
-                             entryRow, entryWeight, weights, out, outDtype: int, stream=None, check: bool = True) -> int:
+                       entryRow, entryWeight, weights, out, outDtype: int, stream=None, check: bool = True) -> int:
     return prepare_expert_linear(numExperts, numCols, hiddenDim, maxEntries, numRows, rows, offsets, entryRow,
-                                       entryWeight, weights, out, outDtype)(stream, check)
+                                 entryWeight, weights, out, outDtype)(stream, check)
 
 
 def epdc_expert_rows_grad(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, dOut, offsets, entryRow,
@@ -131,17 +131,17 @@ def epdc_expert_gate_grad(numExperts: int, cols: int, maxEntries: int, dtype: in
 
 
 def epdc_int_quantize(numWindows: int, rowsPerWindow: int, cols: int, dtype: int, x, rowCount, q, scales, stream=None,
-                       check: bool = True) -> int:
+                      check: bool = True) -> int:
     return prepare_int_quantize(numWindows, rowsPerWindow, cols, dtype, x, rowCount, q, scales)(stream, check)
 
 
 def epdc_expert_gate_int(numExperts: int, cols: int, maxEntries: int, dtype: int, h, offsets, entryWeight, q, scales,
-                          stream=None, check: bool = True) -> int:
+                         stream=None, check: bool = True) -> int:
     return prepare_expert_gate_int(numExperts, cols, maxEntries, dtype, h, offsets, entryWeight, q, scales)(stream, check)
 
 
 def epdc_expert_linear_int(numExperts: int, numCols: int, hiddenDim: int, maxEntries: int, numRows: int, rows, rowScales,
-                             offsets, entryRow, entryWeight, weights, weightScales, out, outDtype: int, stream=None,
-                             check: bool = True) -> int:
+                           offsets, entryRow, entryWeight, weights, weightScales, out, outDtype: int, stream=None,
+                           check: bool = True) -> int:
     return prepare_expert_linear_int(numExperts, numCols, hiddenDim, maxEntries, numRows, rows, rowScales, offsets, entryRow,
-                                       entryWeight, weights, weightScales, out, outDtype)(stream, check)
+                                     entryWeight, weights, weightScales, out, outDtype)(stream, check)

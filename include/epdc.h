@@ -541,9 +541,9 @@ int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, 
  * epdc_expert_product.
  */
 int epdc_expert_linear(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
-                             int32_t numRows, const void *rows, const int32_t *offsets, const int32_t *entryRow,
-                             const float *entryWeight, const void *weights, void *out, int32_t outDtype,
-                             void *stream);
+                       int32_t numRows, const void *rows, const int32_t *offsets, const int32_t *entryRow,
+                       const float *entryWeight, const void *weights, void *out, int32_t outDtype,
+                       void *stream);
 
 /*
  * The gradient of the product's rows, one row per entry:
@@ -625,7 +625,7 @@ int epdc_expert_gate_grad(int32_t numExperts, int32_t cols, int32_t maxEntries, 
  * codes 0.
  */
 int epdc_int_quantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, int32_t dtype, const void *x,
-                       const int32_t *rowCount, void *q, float *scales, void *stream);
+                      const int32_t *rowCount, void *q, float *scales, void *stream);
 
 /*
  * epdc_expert_gate, quantised: the row's values w_i g s(g) u, each taken in 64
@@ -635,7 +635,7 @@ int epdc_int_quantize(int32_t numWindows, int32_t rowsPerWindow, int32_t cols, i
  * exponential rounds.)
  */
 int epdc_expert_gate_int(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
-                          const int32_t *offsets, const float *entryWeight, void *q, float *scales, void *stream);
+                         const int32_t *offsets, const float *entryWeight, void *q, float *scales, void *stream);
 
 /*
  * epdc_expert_linear of int8 rows and weights:
@@ -645,9 +645,9 @@ int epdc_expert_gate_int(int32_t numExperts, int32_t cols, int32_t maxEntries, i
  * [numRows], weightScales [numExperts][numCols] fp32.  Codes may be any int8.
  */
 int epdc_expert_linear_int(int32_t numExperts, int32_t numCols, int32_t hiddenDim, int32_t maxEntries,
-                             int32_t numRows, const void *rows, const float *rowScales, const int32_t *offsets,
-                             const int32_t *entryRow, const float *entryWeight, const void *weights,
-                             const float *weightScales, void *out, int32_t outDtype, void *stream);
+                           int32_t numRows, const void *rows, const float *rowScales, const int32_t *offsets,
+                           const int32_t *entryRow, const float *entryWeight, const void *weights,
+                           const float *weightScales, void *out, int32_t outDtype, void *stream);
 
 /* Message for the last failing call on this thread ("" if none).  The
  * pointer stays valid until the next epdc_* call on the same thread.  MORI
