@@ -175,22 +175,34 @@ enum DenseKind { kDenseProduct, kDenseRowsGrad, kDenseWeightsGrad };
 enum DenseForm { kDenseStream16, kDenseStream64, kDenseTiles128, kDenseTiles256 };
 
 // Which kernel, from the entries that can occur (the groups' sizes are known on
-// the device only).  Times in us, bf16, 7168 -> 4096 unless stated:
+// the device only).  Times in us, bf16 / int8, groups of equal size, weights from
+// memory (one to four experts' stay in the cache from call to call where nothing
+// else runs: tiles then take 76 / 42 for one expert, the streaming forms as here),
+// 7168 -> 4096 unless stated:
 //   * weights streamed where 128x128 tiles would leave CUs idle and experts have
-//     few entries: one expert, 16 / 64 entries 28 / 49 against 105 with tiles; 8
-//     experts, 64 entries 97 against 118; but 32 experts, 64 entries 352 against
-//     307.  Tiles of 64 entries beyond 16 an expert: 2 experts, 64 entries 39
-//     against 50 with 16; 4 experts, 128 entries 73 against 97 (128x128: 109); but
-//     8 experts, 256 entries 142 against 120 with 128x128; one expert, 256 / 512
-//     entries 87 / 173 against 105;
+//     few entries: one expert, 16 entries 28 / 16, 64 entries 49 / 27 against 106 /
+//     57 with tiles; 8 experts, 64 entries 98 / 51 against 120 / 64; 9 experts, 72
+//     entries 122 / 64 against 125 / 68 (10 experts, 80 entries, beyond the border:
+//     125 / 65 against 129 / 69); 16 experts, 128 entries 200 / 102 against 159 / 86;
+//     32 experts, 64 entries 352 / 179 against 308 / 162.  Tiles of 64 entries beyond
+//     16 an expert: 2 experts, 64 entries 39 / 22 against 51 / 28 with 16; 4 experts,
+//     128 entries 74 / 39 against 97 / 51 (128x128: 111 / 59); but 8 experts, 256
+//     entries 143 / 73 against 121 / 65 with 128x128; one expert, 256 entries 87 / 46
+//     against 108 / 58, 512 entries 173 / 89 against 107 / 57;
 //   * 256x256 tiles where the mean group fills a good part of one and there is
-//     one for every CU: 8 experts, 4096 / 2048 entries 219 / 202 against 284 /
-//     159; 32 experts, 4096 entries 419 against 385; 32 experts, 2048 -> 7168,
-//     8192 entries 293 against 324; one expert, 8192 / 2048 entries 357 / 138
-//     against 427 / 113;
+//     one for every CU: 8 experts, 4096 entries 220 / 122 against 284 / 152, 2048
+//     entries 204 / 109 against 162 / 88; 32 experts, 4096 entries 414 / 225 against
+//     384 / 211; 32 experts, 2048 -> 7168, 8192 entries 290 / 157 against 321 / 186;
+//     one expert, 8192 entries 387 / 205 against 485 / 267, 2048 entries 173 / 94
+//     against 130 / 72.  Groups whose sizes differ (entries dealt out at random) need
+//     more tiles of 128 rows, and the border lies lower: 8 experts, 2048 entries 203 /
+//     110 with 256x256 against 250 / 130, 32 experts, 4096 entries 421 / 229 against
+//     512 / 266, both beyond what the rule takes; 8 experts, 4096 entries 376 / 193
+//     against 368 / 192;
 //   * the weights' gradient likewise (its tiles are all there, whatever the
-//     groups): 16 experts, 1024 x 1024, 256 tiles: 16384 / 333 entries 39 / 15.5
-//     against 47 / 16.3; 32 experts, 7168 -> 4096, 4096 entries, fp32 759 against 1057.
+//     groups), bf16 rows: 16 experts, 1024 x 1024, 256 tiles: 16384 / 333 entries 41 /
+//     16.6 against 49 / 17.4; 32 experts, 7168 -> 4096, 4096 entries, fp32 764 against
+//     1071.
 inline DenseForm plan_dense(DenseKind kind, int32_t E, int32_t N, int32_t H, int32_t maxEntries) {
     const int32_t columns = kind == kDenseProduct ? N : H;
     if (kind == kDenseWeightsGrad)

@@ -6,13 +6,16 @@
 //
 // Tiles of 256 x 256 or 128 x 128 of the output, through LDS, with
 // v_mfma_f32_32x32x16_bf16 (v_mfma_i32_32x32x32_i8: the same bytes a lane);
-// plan_dense chooses.  32768 entries of 32 experts, 7168 -> 4096: bf16 1.69 ms,
-// 1.14 PFLOP/s, int8 0.84 ms, 2.3 POP/s (a loop of the instruction alone 1.78 and
-// 3.5), the matrix cores busy 71% of the time at a clock of 1.65 GHz; one dense
-// product of 8192^3 1.36 PFLOP/s.  Rows' gradient, 16384 entries, 7168 -> 2048:
-// 0.53 ms.  Weights' gradient, 16384 entries, 4096 x 7168: 1.17 ms, bound by the
-// results' stores between tiles of eight steps (0.95 without them).
-// 64 entries of 32 experts, bound by the weights: 281 us, 5.8 TB/s.
+// plan_dense chooses.  The kernel's time, median (least) of 40 passes under load:
+// 32768 entries of 32 experts, 7168 -> 4096, groups of different sizes: bf16 1.76
+// (1.73) ms, 1.09 PFLOP/s, int8 0.87 (0.85) ms, 2.2 POP/s (a loop of the
+// instruction alone 1.78 and 3.5), the matrix cores busy 71% of the time at a
+// clock of 1.65 GHz; one dense product of 8192^3 1.36 PFLOP/s.  Rows' gradient,
+// 16384 entries, 7168 -> 2048: 0.56 (0.53) ms.  Weights' gradient, 16384 entries,
+// 4096 x 7168: 1.20 (1.18) ms, bound by the results' stores between tiles of eight
+// steps (0.95 without them).  64 entries of 32 experts, bound by the weights: 283
+// (272) us, 5.8 TB/s.  (Of 20 passes that begin on an idle card, whose clocks are
+// still rising, the same kernels take up to a seventh longer.)
 #pragma once
 
 #include "tiles.h"
@@ -587,8 +590,8 @@ __global__ __launch_bounds__(256, BM *BN > 128 * 128 ? 1 : 2) void dense_tile_ke
             const_cast<uint8_t *>(KIND == kDenseWeightsGrad && P.base ? P.base + (base - P.out) : base), 0, bytes, 0x00020000);
         const int ln = fresh(), low = ln & 31, high = ln >> 5;
         // Where a lane stores: rows low % 16 and 16 behind, 16 bytes; a row's four lanes hold 64 bytes that follow one
-        // another (lanes that each stored their own sums would write 32 at a time: 333 entries' weights' gradient, fp32, 50
-        // against 45 us).
+        // another (lanes that each stored their own sums would write 32 at a time: a tenth slower at the weights' gradient
+        // of 333 entries, 16 experts of 1024 x 1000, fp32).
         constexpr int kRuns = OUT32 ? 2 : 1;  // of 64 bytes in a fragment's row
         const int32_t outside = 0x7ffffff0, mineC = T.c0 + wc + high * (OUT32 ? 4 : 8) + (low >> 4) * (OUT32 ? 8 : 16);
         int32_t at[FC][kRuns];

@@ -519,8 +519,13 @@ int epdc_expert_product(int32_t numExperts, int32_t numCols, int32_t hiddenDim, 
  * dense; rows, weights, gradients and outputs are 16-byte aligned, the other
  * arrays 4-byte.  Products of bf16 values are summed in fp32, in an order that
  * is fixed for given sizes (results are the same from run to run), and rounded
- * once (nearest, ties to even).  maxEntries is best the number of entries that
- * can occur: it chooses the kernel.
+ * once (nearest, ties to even).
+ * maxEntries also chooses the kernel of a product or of its rows' gradient (the
+ * groups' sizes are known on the device only): pass the number of entries that can
+ * occur, not a far larger capacity.  Eight times the number costs 64 entries of
+ * one expert, 7168 -> 4096, twice the time and 8 entries of 32 experts half as
+ * much again; where groups are large and differ in size it can also gain up to a
+ * quarter.
  *
  * The weight of an entry (its token's routing weight) can be applied once, in
  * epdc_expert_gate: the second product then needs none, nor do its gradients,

@@ -1,5 +1,6 @@
 """Groups of more than 2^28 entries: the weights' gradient goes over them to
-the end, and not past it.  Whole numbers, whose sums fp32 holds exactly."""
+the end, and not past it (whole numbers, whose sums fp32 holds exactly).  And
+the activation in codes of more rows than a grid has blocks for."""
 import pytest
 import torch
 
