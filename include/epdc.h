@@ -593,8 +593,9 @@ int epdc_expert_weights_grad(int32_t numExperts, int32_t numCols, int32_t hidden
  * EPDC_MAX_EXPERT_DIM.  Rows i in [offsets[0], offsets[numExperts]) (clamped to
  * [0, maxEntries]; offsets NULL: all) are read and written.  entryWeight
  * [maxEntries] fp32 is w_i (NULL: 1).  out [maxEntries][cols] of outDtype.
- * Computed in fp32 and rounded once.  NaN and infinities propagate as the
- * formula's operations do (g = -inf gives NaN).
+ * Computed in fp32, ((g s(g)) u) w_i from the left, and rounded once.  NaN and
+ * infinities propagate as these operations do (g = -inf gives NaN; a product beyond
+ * fp32's range on the way is infinite, whatever w_i makes of it).
  */
 int epdc_expert_gate(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
                      const int32_t *offsets, const float *entryWeight, void *out, int32_t outDtype, void *stream);
@@ -604,6 +605,7 @@ int epdc_expert_gate(int32_t numExperts, int32_t cols, int32_t maxEntries, int32
  * dH [maxEntries][2 cols] of dtype holds w_i dOut u s (1 + g (1 - s)), then
  * w_i dOut g s; dEntryWeight [maxEntries] fp32 (or NULL: not wanted) the sum of
  * dOut g s u over a row, in an order that is fixed for given cols.  entryWeight NULL: 1.
+ * In fp32 as above, w_i dOut before the other factors.
  */
 int epdc_expert_gate_grad(int32_t numExperts, int32_t cols, int32_t maxEntries, int32_t dtype, const void *h,
                           const int32_t *offsets, const float *entryWeight, const void *dOut, int32_t outDtype,
